@@ -1,4 +1,4 @@
-"""ctypes binding of libgkd (include/gkd.h), one Python function per C entry point.
+"""ctypes binding of libgkd (include/gkd.h, include/gkd_blocks.h), one Python function per C entry point.
 
 Argument marshalling only: every function here turns tensors into device
 pointers and sizes, calls the C ABI, and raises GkdError on a non-OK status.
@@ -17,6 +17,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "gkd.h")
 
 GKD_OK, GKD_ERR_ARG, GKD_ERR_SHAPE, GKD_ERR_DTYPE, GKD_ERR_ALIGN, GKD_ERR_CUDA, GKD_ERR_TIMEOUT = range(7)
 GKD_F32, GKD_BF16 = 0, 1
+GKD_ACT_NONE, GKD_ACT_RELU, GKD_ACT_GELU, GKD_ACT_QUICK_GELU = range(4)
 STATUS_NAMES = {0: "GKD_OK", 1: "GKD_ERR_ARG", 2: "GKD_ERR_SHAPE", 3: "GKD_ERR_DTYPE", 4: "GKD_ERR_ALIGN",
                 5: "GKD_ERR_CUDA", 6: "GKD_ERR_TIMEOUT"}
 DEBUG_SKIP_PRODUCER_ARRIVE = 1
@@ -39,6 +40,15 @@ _ll = ctypes.c_longlong
 _f = ctypes.c_float
 _u = ctypes.c_uint
 
+
+
+class GkdHeads(ctypes.Structure):
+    """gkd_heads of gkd_blocks.h: heads of a batch of rows, strides in elements."""
+    _fields_ = [("data", _p), ("batch_stride", _ll), ("row_stride", _ll), ("head_stride", _ll), ("heads", _i)]
+
+
+_h = ctypes.POINTER(GkdHeads)
+
 _SIGS = {
     "gkd_pool_prototypes": [_p, _i, _i, _i, _i, _i, _p, _p, _i, _f, _f, _p, _ll, _p],
     "gkd_norm_kernels": [_p, _p, _i, _i, _i, _i, _f, _i, _p, _p],
@@ -50,6 +60,9 @@ _SIGS = {
     "gkd_preprocess": [_p, _i, _i, _p, _i, _i, _p, _p],
     "gkd_heatmap_contract_first": [_p, _i, _i, _i, _i, _i, _i, _p, _ll, _p, _ll, _i, _i, _p, _p, _p],
     "gkd_roi_to_image": [_p, _p, _i, _i, _i, _p, _p],
+    "gkd_linear": [_p, _i, _i, _i, _ll, _p, _i, _p, _i, _p, _p, _ll, _p, _i, _ll, _p],
+    "gkd_qk_norm_rope": [_h, _h, _i, _i, _i, _i, _p, _p, _f, _p, _ll, _i, _p, _p, _i, _i, _h, _h, _p],
+    "gkd_attention": [_h, _h, _h, _i, _i, _i, _i, _i, _f, _i, _p, _ll, _h, _p],
     "gkd_check_device_error": [_p],
     "gkd_set_wait_timeout_ms": [_u],
     "gkd_debug_set_flags": [_u],
@@ -176,3 +189,36 @@ def gkd_heatmap_contract_first(feat, fdt, B, h, w, C, up, kern, kern_batch_strid
     _check("gkd_heatmap_contract_first", lib.gkd_heatmap_contract_first(
         _ptr(feat), fdt, B, h, w, C, up, _ptr(kern), kern_batch_stride, _ptr(mask), mask_batch_stride, M, K,
         _ptr(scratch), _ptr(heat), _stream(stream, feat)))
+
+
+def gkd_heads(x) -> GkdHeads | None:
+    """The gkd_heads view of a tensor [B][rows][heads][D] (any strides, last axis contiguous); views and None pass."""
+    if x is None or isinstance(x, GkdHeads):
+        return x
+    strides = x.stride()
+    if len(strides) != 4 or (strides[3] != 1 and x.shape[3] > 1):
+        raise GkdError(GKD_ERR_SHAPE, "gkd_heads", "a view is [B][rows][heads][D] with contiguous D")
+    return GkdHeads(x.data_ptr(), strides[0], strides[1], strides[2], x.shape[2])
+
+
+def gkd_linear(x, dt, T, Cin, x_stride, weight, Cout, bias, act, scale, residual, residual_stride, out, out_dt,
+               out_stride, stream=None):
+    _check("gkd_linear", lib.gkd_linear(
+        _ptr(x), dt, T, Cin, x_stride, _ptr(weight), Cout, _ptr(bias), act, _ptr(scale), _ptr(residual),
+        residual_stride, _ptr(out), out_dt, out_stride, _stream(stream, x)))
+
+
+def gkd_qk_norm_rope(q, k, dt, B, T, D, q_weight, k_weight, eps, pos, pos_batch_stride, axes, pair_axis, pair_freq,
+                     pairs, interleaved, q_out, k_out, stream=None):
+    """q, k, q_out and k_out: tensors [B][T][heads][D], or GkdHeads views."""
+    _check("gkd_qk_norm_rope", lib.gkd_qk_norm_rope(
+        gkd_heads(q), gkd_heads(k), dt, B, T, D, _ptr(q_weight), _ptr(k_weight), eps, _ptr(pos), pos_batch_stride,
+        axes, _ptr(pair_axis), _ptr(pair_freq), pairs, interleaved, gkd_heads(q_out), gkd_heads(k_out),
+        _stream(stream, q)))
+
+
+def gkd_attention(q, k, v, dt, B, Tq, Tk, D, scale, causal, key_mask, key_mask_batch_stride, out, stream=None):
+    """q, k, v and out: tensors [B][rows][heads][D], or GkdHeads views."""
+    _check("gkd_attention", lib.gkd_attention(
+        gkd_heads(q), gkd_heads(k), gkd_heads(v), dt, B, Tq, Tk, D, scale, causal, _ptr(key_mask),
+        key_mask_batch_stride, gkd_heads(out), _stream(stream, q)))

@@ -1,14 +1,16 @@
-// C ABI of libgkd (declared in include/gkd.h): host-side argument validation,
+// C ABI of libgkd (declared in include/gkd.h and include/gkd_blocks.h): host-side argument validation,
 // device selection, per-device state and kernel launches. Checks that need no
 // CUDA call (null pointers, sizes, dtypes, alignment) run first, so a bad call
 // is rejected before the runtime is touched.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
 #include <string>
 
 #include "../../include/gkd.h"
+#include "../../include/gkd_blocks.h"
 #include "gkd_internal.h"
 
 namespace {
@@ -510,6 +512,253 @@ gkd_status gkd_heatmap_decode_noalloc(const void* feat, gkd_dtype fdt, int B, in
   GKD_TRY(device_state(dev, &ds));
   return enqueue_heatmap_decode(dev, feat, fdt, B, h, w, C, kern, kdt, kern_batch_stride, mask, mask_batch_stride,
                                 M, K, ds->noalloc_keys, xy, score, idx, valid, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Operators of the transformer blocks (gkd_blocks.h)
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr long long kMaxTensorStride = 1ll << 39;   // bytes; a tensor map's strides stay below 2^40
+
+bool known_dtype(gkd_dtype dt) { return dt == GKD_F32 || dt == GKD_BF16; }
+
+// Rows of a [T][n] tensor of `size`-byte elements, `stride` elements apart.
+gkd_status check_rows(const char* name, const void* p, int T, int n, long long stride, int size) {
+  if (!p) return fail(GKD_ERR_ARG, "%s: null tensor pointer", name);
+  if (!aligned16(p)) return fail(GKD_ERR_ALIGN, "%s must be 16-byte aligned", name);
+  if (T < 2) return GKD_OK;
+  if (stride < n) return fail(GKD_ERR_SHAPE, "%s: row stride %lld < %d", name, stride, n);
+  if (stride > kMaxTensorStride / size) return fail(GKD_ERR_SHAPE, "%s: row stride %lld too large", name, stride);
+  if (stride * size % 16) return fail(GKD_ERR_ALIGN, "%s: row stride must be a multiple of 16 bytes", name);
+  return GKD_OK;
+}
+
+// A view's pointer and strides; on success `out` has them with those of axes of size 1 replaced by the dense ones.
+gkd_status check_heads(const char* name, const gkd_heads* v, int B, int T, int D, int size, bool output,
+                       gkd::HeadsView* out) {
+  if (!v->data) return fail(GKD_ERR_ARG, "%s: null tensor pointer", name);
+  if (!aligned16(v->data)) return fail(GKD_ERR_ALIGN, "%s must be 16-byte aligned", name);
+  const char* axis[3] = {"batch", "row", "head"};
+  const long long stride[3] = {v->batch_stride, v->row_stride, v->head_stride};
+  const int extent[3] = {B, T, v->heads};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] < 2) continue;
+    if (stride[i] < D && !(i == 0 && stride[i] == 0 && !output))
+      return fail(GKD_ERR_SHAPE, "%s: %s stride %lld < %d", name, axis[i], stride[i], D);
+    if (stride[i] > kMaxTensorStride / size)
+      return fail(GKD_ERR_SHAPE, "%s: %s stride %lld too large", name, axis[i], stride[i]);
+    if (stride[i] * size % 16)
+      return fail(GKD_ERR_ALIGN, "%s: %s stride must be a multiple of 16 bytes", name, axis[i]);
+  }
+  out->data = v->data;
+  out->heads = v->heads;
+  out->batch_stride = B > 1 ? stride[0] : 0;
+  out->row_stride = T > 1 ? stride[1] : D;
+  out->head_stride = v->heads > 1 ? stride[2] : D;
+  return GKD_OK;
+}
+
+gkd_status check_head_count(const char* name, const gkd_heads* v) {
+  if (!v) return fail(GKD_ERR_ARG, "%s: null view", name);
+  if (v->heads < 1 || v->heads > 1024) return fail(GKD_ERR_SHAPE, "%s: heads=%d out of range [1, 1024]", name, v->heads);
+  return GKD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gkd_status gkd_linear(const void* x, gkd_dtype dt, int T, int Cin, long long x_stride, const void* weight, int Cout,
+                      const float* bias, gkd_activation act, const float* scale, const void* residual,
+                      long long residual_stride, void* out, gkd_dtype out_dt, long long out_stride, void* stream) {
+  if (!known_dtype(dt) || !known_dtype(out_dt)) return fail(GKD_ERR_ARG, "unknown dtype");
+  if (dt == GKD_F32 && out_dt != GKD_F32) return fail(GKD_ERR_DTYPE, "fp32 inputs give an fp32 output");
+  if (act < GKD_ACT_NONE || act > GKD_ACT_QUICK_GELU)
+    return fail(GKD_ERR_ARG, "unknown activation %d", static_cast<int>(act));
+  if (T < 0) return fail(GKD_ERR_SHAPE, "T=%d must not be negative", T);
+  if (Cin < 8 || Cin > 65536 || Cin % 8) return fail(GKD_ERR_SHAPE, "Cin=%d must be a multiple of 8 in [8, 65536]", Cin);
+  if (Cout < 8 || Cout > 65536 || Cout % 8)
+    return fail(GKD_ERR_SHAPE, "Cout=%d must be a multiple of 8 in [8, 65536]", Cout);
+  if (T == 0) return ok();
+  const int size = dt == GKD_BF16 ? 2 : 4, osize = out_dt == GKD_BF16 ? 2 : 4;
+  GKD_TRY(check_rows("x", x, T, Cin, x_stride, size));
+  GKD_TRY(check_rows("weight", weight, Cout, Cin, Cin, size));
+  GKD_TRY(check_rows("out", out, T, Cout, out_stride, osize));
+  if (residual) GKD_TRY(check_rows("residual", residual, T, Cout, residual_stride, osize));
+  if (!aligned16(bias) || !aligned16(scale)) return fail(GKD_ERR_ALIGN, "bias/scale must be 16-byte aligned");
+  int dev = 0;
+  GKD_TRY(use_device_of(x, "x", &dev));
+  GKD_TRY(check_same_device(weight, "weight", dev));
+  GKD_TRY(check_same_device(out, "out", dev));
+  if (bias) GKD_TRY(check_same_device(bias, "bias", dev));
+  if (scale) GKD_TRY(check_same_device(scale, "scale", dev));
+  if (residual) GKD_TRY(check_same_device(residual, "residual", dev));
+  DeviceState* ds = nullptr;
+  GKD_TRY(device_state(dev, &ds));
+  gkd::LinearArgs a{};
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.scale = scale;
+  a.residual = residual;
+  a.out = out;
+  a.x_stride = T > 1 ? x_stride : Cin;
+  a.residual_stride = T > 1 ? residual_stride : Cout;
+  a.out_stride = T > 1 ? out_stride : Cout;
+  a.T = T;
+  a.Cin = Cin;
+  a.Cout = Cout;
+  a.act = act;
+  a.in_bf16 = dt == GKD_BF16;
+  a.out_bf16 = out_dt == GKD_BF16;
+  a.err = ds->err_word;
+  a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
+  const char* why = "";
+  cudaError_t e = gkd::launch_linear(a, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "linear: %s", why);
+  return launched(e, "linear");
+}
+
+gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_dtype dt, int B, int T, int D,
+                            const float* q_weight, const float* k_weight, float eps, const float* pos,
+                            long long pos_batch_stride, int axes, const uint8_t* pair_axis, const float* pair_freq,
+                            int pairs, int interleaved, const gkd_heads* q_out, const gkd_heads* k_out, void* stream) {
+  if (!known_dtype(dt)) return fail(GKD_ERR_ARG, "unknown dtype %d", static_cast<int>(dt));
+  if (B < 0 || B > 65535) return fail(GKD_ERR_SHAPE, "B=%d out of range [0, 65535]", B);
+  if (T < 0) return fail(GKD_ERR_SHAPE, "T=%d must not be negative", T);
+  if (D < 8 || D > 256 || D % 8) return fail(GKD_ERR_SHAPE, "D=%d must be a multiple of 8 in [8, 256]", D);
+  if (axes < 1 || axes > 3) return fail(GKD_ERR_SHAPE, "axes=%d out of range [1, 3]", axes);
+  if (pairs < 0 || pairs > D / 2 || pairs % 4)
+    return fail(GKD_ERR_SHAPE, "pairs=%d must be a multiple of 4 in [0, D / 2]", pairs);
+  if (interleaved != 0 && interleaved != 1) return fail(GKD_ERR_ARG, "interleaved must be 0 or 1");
+  if (pos_batch_stride < 0) return fail(GKD_ERR_SHAPE, "pos_batch_stride must not be negative");
+  GKD_TRY(check_head_count("q", q));
+  GKD_TRY(check_head_count("q_out", q_out));
+  if (q->heads != q_out->heads) return fail(GKD_ERR_SHAPE, "q and q_out differ in heads");
+  if ((k == nullptr) != (k_out == nullptr)) return fail(GKD_ERR_ARG, "k and k_out go together");
+  if (k) {
+    GKD_TRY(check_head_count("k", k));
+    GKD_TRY(check_head_count("k_out", k_out));
+    if (k->heads != k_out->heads) return fail(GKD_ERR_SHAPE, "k and k_out differ in heads");
+  }
+  const bool norm = q_weight != nullptr;
+  if (k && (k_weight != nullptr) != norm) return fail(GKD_ERR_ARG, "q_weight and k_weight go together");
+  if (norm && !(eps > 0.f)) return fail(GKD_ERR_ARG, "eps must be positive");
+  if (B == 0 || T == 0) return ok();
+  if (pairs && (!pos || !pair_axis || !pair_freq)) return fail(GKD_ERR_ARG, "null tensor pointer");
+  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight) |
+       reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(pair_freq)) & 3u)
+    return fail(GKD_ERR_ALIGN, "weights, pos and pair_freq must be 4-byte aligned");
+  const int size = dt == GKD_BF16 ? 2 : 4;
+  gkd::HeadsView in[2] = {}, out[2] = {};
+  GKD_TRY(check_heads("q", q, B, T, D, size, false, &in[0]));
+  GKD_TRY(check_heads("q_out", q_out, B, T, D, size, true, &out[0]));
+  if (k) {
+    GKD_TRY(check_heads("k", k, B, T, D, size, false, &in[1]));
+    GKD_TRY(check_heads("k_out", k_out, B, T, D, size, true, &out[1]));
+  }
+  int dev = 0;
+  GKD_TRY(use_device_of(q->data, "q", &dev));
+  GKD_TRY(check_same_device(q_out->data, "q_out", dev));
+  if (k) {
+    GKD_TRY(check_same_device(k->data, "k", dev));
+    GKD_TRY(check_same_device(k_out->data, "k_out", dev));
+  }
+  if (norm) GKD_TRY(check_same_device(q_weight, "q_weight", dev));
+  if (norm && k) GKD_TRY(check_same_device(k_weight, "k_weight", dev));
+  if (pairs) {
+    GKD_TRY(check_same_device(pos, "pos", dev));
+    GKD_TRY(check_same_device(pair_axis, "pair_axis", dev));
+    GKD_TRY(check_same_device(pair_freq, "pair_freq", dev));
+  }
+  DeviceState* ds = nullptr;
+  GKD_TRY(device_state(dev, &ds));
+  gkd::RopeArgs g{};
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    gkd::RopeSide& s = g.side[i];
+    s.in = in[i].data;
+    s.out = out[i].data;
+    s.in_bs = in[i].batch_stride;
+    s.in_rs = in[i].row_stride;
+    s.in_hs = in[i].head_stride;
+    s.out_bs = out[i].batch_stride;
+    s.out_rs = out[i].row_stride;
+    s.out_hs = out[i].head_stride;
+    s.heads = in[i].heads;
+    s.weight = i ? k_weight : q_weight;
+  }
+  g.B = B;
+  g.T = T;
+  g.D = D;
+  g.axes = axes;
+  g.pairs = pairs;
+  g.interleaved = interleaved;
+  g.eps = eps;
+  g.pos = pos;
+  g.pos_bs = pos_batch_stride;
+  g.pair_axis = pair_axis;
+  g.pair_freq = pair_freq;
+  const cudaError_t e = gkd::launch_qk_norm_rope(g, dt == GKD_BF16, ds->num_sms, static_cast<cudaStream_t>(stream));
+  return launched(e, "qk_norm_rope");
+}
+
+gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads* v, gkd_dtype dt, int B, int Tq, int Tk,
+                         int D, float scale, int causal, const uint8_t* key_mask, long long key_mask_batch_stride,
+                         const gkd_heads* out, void* stream) {
+  if (!known_dtype(dt)) return fail(GKD_ERR_ARG, "unknown dtype %d", static_cast<int>(dt));
+  if (B < 0 || B > 65535) return fail(GKD_ERR_SHAPE, "B=%d out of range [0, 65535]", B);
+  constexpr int kMaxRows = 0x7fffffff - 256;
+  if (Tq < 0 || Tk < 0 || Tq > kMaxRows || Tk > kMaxRows) return fail(GKD_ERR_SHAPE, "Tq=%d Tk=%d out of range", Tq, Tk);
+  if (D < 8 || D > 128 || D % 8) return fail(GKD_ERR_SHAPE, "D=%d must be a multiple of 8 in [8, 128]", D);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GKD_ERR_ARG, "scale must be positive and finite");
+  if (causal != 0 && causal != 1) return fail(GKD_ERR_ARG, "causal must be 0 or 1");
+  if (key_mask_batch_stride < 0) return fail(GKD_ERR_SHAPE, "key_mask_batch_stride must not be negative");
+  GKD_TRY(check_head_count("q", q));
+  GKD_TRY(check_head_count("k", k));
+  GKD_TRY(check_head_count("v", v));
+  GKD_TRY(check_head_count("out", out));
+  if (q->heads != out->heads) return fail(GKD_ERR_SHAPE, "q and out differ in heads");
+  if (k->heads != v->heads || q->heads % k->heads)
+    return fail(GKD_ERR_SHAPE, "k and v must have the same heads, a divisor of q's");
+  if (B == 0 || Tq == 0) return ok();
+  const int size = dt == GKD_BF16 ? 2 : 4;
+  gkd::AttentionArgs a{};
+  GKD_TRY(check_heads("q", q, B, Tq, D, size, false, &a.q));
+  GKD_TRY(check_heads("out", out, B, Tq, D, size, true, &a.out));
+  if (Tk > 0) {
+    GKD_TRY(check_heads("k", k, B, Tk, D, size, false, &a.k));
+    GKD_TRY(check_heads("v", v, B, Tk, D, size, false, &a.v));
+  }
+  a.k.heads = k->heads;
+  if ((static_cast<long long>(Tq) + 63) / 64 * q->heads * B > 0x7fffffffll)
+    return fail(GKD_ERR_SHAPE, "too many query tiles (B=%d, heads=%d, Tq=%d)", B, q->heads, Tq);
+  int dev = 0;
+  GKD_TRY(use_device_of(q->data, "q", &dev));
+  GKD_TRY(check_same_device(out->data, "out", dev));
+  if (Tk > 0) {
+    GKD_TRY(check_same_device(k->data, "k", dev));
+    GKD_TRY(check_same_device(v->data, "v", dev));
+    if (key_mask) GKD_TRY(check_same_device(key_mask, "key_mask", dev));
+  }
+  DeviceState* ds = nullptr;
+  GKD_TRY(device_state(dev, &ds));
+  a.B = B;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.D = D;
+  a.causal = causal;
+  a.scale = scale;
+  a.mask = key_mask;
+  a.mask_batch_stride = key_mask_batch_stride;
+  a.err = ds->err_word;
+  a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
+  const char* why = "";
+  const cudaError_t e = gkd::launch_attention(a, dt == GKD_BF16, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "attention: %s", why);
+  return launched(e, "attention");
 }
 
 }  // extern "C"

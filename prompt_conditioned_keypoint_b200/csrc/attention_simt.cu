@@ -1,0 +1,195 @@
+// gkd_attention on the fp32 units: out = softmax(scale q k^T) v under a key mask.
+//
+// One CTA per (batch, head, 64 query rows). Keys come 64 at a time: a thread has
+// 4 rows x 8 keys of the scores and 4 rows x (D / 8) columns of the output, with
+// the running maximum and sum of its rows (the eight threads of a row group agree
+// on them by shuffles). Scores are kept in units of log 2. Key tiles that the
+// mask or the diagonal leaves empty are skipped; hidden keys and values are
+// replaced by zeros on their way into shared memory, so what they hold never
+// meets a product.
+#include "blocks_common.cuh"
+#include "gkd_internal.h"
+
+namespace gkd {
+namespace att {
+
+constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+
+template <typename T, int DC>   // DC: head columns in units of 32, rounded up
+__global__ void __launch_bounds__(kThreads) attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
+  extern __shared__ float sm[];
+  constexpr int DP = 32 * DC + 4;
+  float* qs = sm;
+  float* ks = qs + kRows * DP;
+  float* vs = ks + kKeys * DP;
+  float* ps = vs + kKeys * DP;                       // [64][68]
+  __shared__ uint8_t ok[kKeys];
+  const int tid = threadIdx.x, rg = tid >> 3, cg = tid & 7;
+  const int ntiles = (a.Tq + kRows - 1) / kRows;
+  const int tile = blockIdx.x % ntiles;
+  const int bh = blockIdx.x / ntiles, h = bh % a.q.heads, b = bh / a.q.heads;
+  const int hk = h / (a.q.heads / a.k.heads);
+  const int r0 = tile * kRows;
+  const T* q = static_cast<const T*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
+  const T* k = static_cast<const T*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
+  const T* v = static_cast<const T*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
+  T* o = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride;
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
+  const int nq4 = a.D / 4;
+  const float qscale = a.scale * 1.4426950408889634f;
+  for (int e = tid; e < kRows * 8 * DC; e += kThreads) {
+    const int r = e / (8 * DC), c = e % (8 * DC);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < a.Tq && c < nq4) x = load4(q + (r0 + r) * a.q.row_stride + 4 * c);
+    *reinterpret_cast<float4*>(qs + r * DP + 4 * c) = x;
+  }
+  float m[4], l[4], acc[4][4 * DC];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4 * DC; ++c) acc[i][c] = 0.f;
+  }
+  const long long shift = static_cast<long long>(a.Tk) - a.Tq;   // causal: key j for row i iff j <= i + shift
+  long long klast = a.Tk;
+  if (a.causal) klast = min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift);
+  for (long long k0 = 0; k0 < klast; k0 += kKeys) {
+    bool mine = false;
+    if (tid < kKeys) {
+      mine = k0 + tid < a.Tk && (!mask || mask[k0 + tid] != 0);
+    }
+    const int any = __syncthreads_or(mine);
+    if (!any) continue;
+    if (tid < kKeys) ok[tid] = mine;
+    __syncthreads();
+    for (int e = tid; e < kKeys * 8 * DC; e += kThreads) {
+      const int r = e / (8 * DC), c = e % (8 * DC);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (ok[r] && c < nq4) {
+        x = load4(k + (k0 + r) * a.k.row_stride + 4 * c);
+        y = load4(v + (k0 + r) * a.v.row_stride + 4 * c);
+      }
+      *reinterpret_cast<float4*>(ks + r * DP + 4 * c) = x;
+      *reinterpret_cast<float4*>(vs + r * DP + 4 * c) = y;
+    }
+    __syncthreads();
+    float s[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
+    for (int c = 0; c < nq4; ++c) {
+      float4 qv[4], kv[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (4 * rg + i) * DP + 4 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (cg + 8 * j) * DP + 4 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long row = r0 + 4 * rg + i;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool live = ok[cg + 8 * j] && (!a.causal || k0 + cg + 8 * j <= row + shift);
+        s[i][j] = live ? s[i][j] * qscale : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: every weight is 0
+      const float f = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        ps[(4 * rg + i) * 68 + cg + 8 * j] = p;
+      }
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l[i] = l[i] * f + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < 4 * DC; ++c) acc[i][c] *= f;
+    }
+    __syncwarp();                                                 // a row's weights come from its own warp
+#pragma unroll 4
+    for (int j4 = 0; j4 < kKeys / 4; ++j4) {
+      float4 pv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (4 * rg + i) * 68 + 4 * j4);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+        for (int d = 0; d < DC; ++d) {
+          const float4 x = *reinterpret_cast<const float4*>(vs + (4 * j4 + jj) * DP + 32 * d + 4 * cg);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = jj == 0 ? pv[i].x : jj == 1 ? pv[i].y : jj == 2 ? pv[i].z : pv[i].w;
+            acc[i][4 * d] = fmaf(p, x.x, acc[i][4 * d]);
+            acc[i][4 * d + 1] = fmaf(p, x.y, acc[i][4 * d + 1]);
+            acc[i][4 * d + 2] = fmaf(p, x.z, acc[i][4 * d + 2]);
+            acc[i][4 * d + 3] = fmaf(p, x.w, acc[i][4 * d + 3]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long row = r0 + 4 * rg + i;
+    if (row >= a.Tq) continue;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+    for (int d = 0; d < DC; ++d)
+      if (32 * d + 4 * cg < a.D)
+        store4(o + row * a.out.row_stride + 32 * d + 4 * cg,
+               make_float4(acc[i][4 * d] * inv, acc[i][4 * d + 1] * inv, acc[i][4 * d + 2] * inv,
+                           acc[i][4 * d + 3] * inv));
+  }
+}
+
+template <typename T, int DC>
+cudaError_t go(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
+  constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * 68);
+  cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  attention_simt_kernel<T, DC><<<grid, kThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pick(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
+  switch ((a.D + 31) / 32) {
+    case 1:
+      return go<T, 1>(a, grid, stream);
+    case 2:
+      return go<T, 2>(a, grid, stream);
+    case 3:
+      return go<T, 3>(a, grid, stream);
+    default:
+      return go<T, 4>(a, grid, stream);
+  }
+}
+
+}  // namespace att
+
+cudaError_t launch_attention(AttentionArgs& a, bool bf16, cudaStream_t stream, const char** why) {
+  (void)why;
+  const long long ntiles = (static_cast<long long>(a.Tq) + att::kRows - 1) / att::kRows;
+  const long long grid = ntiles * a.q.heads * a.B;
+  return bf16 ? att::pick<__nv_bfloat16>(a, static_cast<unsigned>(grid), stream)
+              : att::pick<float>(a, static_cast<unsigned>(grid), stream);
+}
+
+}  // namespace gkd

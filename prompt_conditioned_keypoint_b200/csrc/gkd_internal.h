@@ -105,6 +105,59 @@ cudaError_t launch_pool_tc(const float* support, int B, int h, int w, int C, con
                            long long proto_batch_stride, unsigned* err, unsigned long long wait_limit_ns,
                            int num_sms, cudaStream_t stream, const char** why);
 
+// ---------------------------------------------------------------------------
+// Operators of the transformer blocks (gkd_blocks.h)
+// ---------------------------------------------------------------------------
+struct LinearArgs {
+  const void* x;
+  const void* weight;        // [Cout][Cin]
+  const float* bias;         // [Cout] or null
+  const float* scale;        // [Cout] or null
+  const void* residual;      // of the output's type, or null
+  void* out;
+  long long x_stride, residual_stride, out_stride;   // elements between rows
+  int T, Cin, Cout, act;
+  bool in_bf16, out_bf16;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+cudaError_t launch_linear(LinearArgs& a, cudaStream_t stream, const char** why);
+
+struct RopeSide {            // q or k
+  const void* in;
+  void* out;
+  long long in_bs, in_rs, in_hs, out_bs, out_rs, out_hs;   // elements between batches, rows, heads
+  int heads;                 // 0: no such side
+  const float* weight;       // [D] or null (no norm)
+};
+struct RopeArgs {
+  RopeSide side[2];
+  int B, T, D, axes, pairs, interleaved;
+  float eps;
+  const float* pos;          // [T][axes] per batch
+  long long pos_bs;
+  const uint8_t* pair_axis;
+  const float* pair_freq;
+  int tok, log_lanes;        // set by the launcher: rows per CTA, log2 of the lanes per head
+};
+cudaError_t launch_qk_norm_rope(RopeArgs& g, bool bf16, int num_sms, cudaStream_t stream);
+
+struct HeadsView {           // element (b, t, h, i) at data + b batch_stride + t row_stride + h head_stride + i
+  void* data;
+  long long batch_stride, row_stride, head_stride;
+  int heads;
+};
+struct AttentionArgs {
+  HeadsView q, k, v, out;
+  int B, Tq, Tk, D, causal;
+  float scale;
+  const uint8_t* mask;       // batch b's [Tk] at mask + b * mask_batch_stride, or null
+  long long mask_batch_stride;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+cudaError_t launch_attention(AttentionArgs& a, bool bf16, cudaStream_t stream, const char** why);
+
 // cuTensorMapEncodeTiled resolved through the runtime's driver entry point.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
