@@ -617,7 +617,7 @@ gkd_status gkd_linear(const void* x, gkd_dtype dt, int T, int Cin, long long x_s
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
   const char* why = "";
-  cudaError_t e = gkd::launch_linear(a, static_cast<cudaStream_t>(stream), &why);
+  cudaError_t e = gkd::launch_linear(a, ds->num_sms, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "linear: %s", why);
   return launched(e, "linear");
 }

@@ -121,7 +121,8 @@ struct LinearArgs {
   unsigned* err;
   unsigned long long wait_limit_ns;
 };
-cudaError_t launch_linear(LinearArgs& a, cudaStream_t stream, const char** why);
+cudaError_t launch_linear(LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);
+cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16 operands
 
 struct RopeSide {            // q or k
   const void* in;

@@ -1,4 +1,4 @@
-// gkd_linear: out = residual + scale * act(x weight^T + bias).
+// gkd_linear on the fp32 units, fp32 operands: out = residual + scale * act(x weight^T + bias).
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
@@ -9,13 +9,12 @@ constexpr int kTile = 64, kStep = 16;
 
 // One 64 x 64 tile of the output per CTA, a 4 x 4 patch per thread; the channels
 // go through shared memory 16 at a time.
-template <typename TI, typename TO>
 __global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ LinearArgs a) {
   __shared__ float xs[kStep][kTile + 4], ws[kStep][kTile + 4];
   const int t0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
   const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
-  const TI* x = static_cast<const TI*>(a.x);
-  const TI* w = static_cast<const TI*>(a.weight);
+  const float* x = static_cast<const float*>(a.x);
+  const float* w = static_cast<const float*>(a.weight);
   float acc[4][4] = {};
   const int lr = tid >> 2, lc = (tid & 3) * 4;
   for (int c0 = 0; c0 < a.Cin; c0 += kStep) {
@@ -45,7 +44,7 @@ __global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ Lin
     if (t >= a.T || n >= a.Cout) continue;                         // Cout is a multiple of 8
     float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.residual)
-      res = load4(static_cast<const TO*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n);
+      res = load4(static_cast<const float*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n);
     const float rv[4] = {res.x, res.y, res.z, res.w};
     float y[4];
 #pragma unroll
@@ -54,21 +53,16 @@ __global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ Lin
       if (a.scale) y[j] *= a.scale[n + j];
       y[j] += rv[j];
     }
-    store4(static_cast<TO*>(a.out) + static_cast<long long>(t) * a.out_stride + n, make_float4(y[0], y[1], y[2], y[3]));
+    store4(static_cast<float*>(a.out) + static_cast<long long>(t) * a.out_stride + n, make_float4(y[0], y[1], y[2], y[3]));
   }
 }
 
 }  // namespace lin
 
-cudaError_t launch_linear(LinearArgs& a, cudaStream_t stream, const char** why) {
-  (void)why;
+cudaError_t launch_linear(LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
+  if (a.in_bf16) return launch_linear_tc(a, num_sms, stream, why);
   const dim3 grid((a.T + lin::kTile - 1) / lin::kTile, (a.Cout + lin::kTile - 1) / lin::kTile);
-  if (!a.in_bf16)
-    lin::linear_kernel<float, float><<<grid, 256, 0, stream>>>(a);
-  else if (a.out_bf16)
-    lin::linear_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-  else
-    lin::linear_kernel<__nv_bfloat16, float><<<grid, 256, 0, stream>>>(a);
+  lin::linear_kernel<<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,624 @@
+// gkd_linear on the tensor cores, bf16 operands:
+//   out = residual + scale * act(x weight^T + bias).
+// Two kernels. Both feed tcgen05.mma from a ring of 64-channel stages that TMA
+// fills (128B-swizzled K-major tiles, zeros past every edge) and accumulate in
+// fp32 in tensor memory.
+//
+//   rows_kernel    many rows: 128 rows x 256 columns per tile, rows on the lanes.
+//                  One CTA per SM walks over the tiles; two accumulators, so that
+//                  the next tile's products run under this tile's epilogue.
+//   split_kernel   few rows: 128 columns (the weights, which are the large operand,
+//                  on the lanes) x N <= 128 rows per tile; a cluster of S CTAs
+//                  shares a tile's channels, and their partial sums meet in
+//                  shared memory (rank order, so the result is always the same).
+//
+// The tensor core truncates each K = 16 step's sum, so a sum of Cin products
+// drifts towards zero by about Cin / 32 of 2^-23 (measured: 1.0e-6 of the result
+// at 1024 channels, 4.4e-6 at 4096, against 6e-7 for fp32 fused multiply-adds).
+// A bf16 output does not see that; for an fp32 output sums of at most 512
+// channels stay in the accumulator and are added up by the epilogue in fp32.
+#include "blocks_common.cuh"
+#include "gkd_internal.h"
+
+namespace gkd {
+namespace lintc {
+
+constexpr int kChunk = 64;                         // channels per stage: one 128-byte row of bf16
+constexpr int kFlush = 8;                          // stages per accumulator for fp32 outputs (512 channels)
+
+__device__ __forceinline__ uint32_t idesc_bf16(int n) {   // fp32 accumulator, bf16 x bf16, both K-major, M = 128
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
+constexpr int kM = 128, kN = 256;
+constexpr int kABytes = kM * 128, kBBytes = kN * 128, kStageBytes = kABytes + kBBytes;
+constexpr int kEpiWarps = 8, kWarps = 2 + kEpiWarps, kThreads = 32 * kWarps;
+constexpr int kBufBytes = 4096;                    // 32 rows x 128 bytes of output (or residual), per epilogue warp
+
+// With a residual a warp keeps two buffers (one being loaded while the other is
+// worked on) and the ring gives up a stage for them.
+template <bool RES>
+struct Ring {
+  static constexpr int kStages = RES ? 3 : 4, kBufs = RES ? 2 : 1;
+  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * kBufs * kBufBytes + 512;
+};
+
+struct RowsArgs {
+  CUtensorMap x, w, out, res;
+  const float* bias;
+  const float* scale;
+  int T, Cin, Cout, act;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+
+struct RowsCtl {
+  uint64_t full[4], empty[4], accfull[2], accempty[2], res[kEpiWarps][2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(RowsCtl) <= 512, "control block");
+
+template <bool F32OUT, bool RES>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ RowsArgs a) {
+  using R = Ring<RES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* bufs = smem + R::kStages * kStageBytes;
+  RowsCtl* ctl = reinterpret_cast<RowsCtl*>(bufs + kEpiWarps * R::kBufs * kBufBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ncol = (a.Cout + kN - 1) / kN;
+  const long long ntiles = static_cast<long long>((a.T + kM - 1) / kM) * ncol;
+  const int nk = (a.Cin + kChunk - 1) / kChunk;
+  const int flush = F32OUT ? kFlush : nk;            // stages per accumulator
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abortp = &ctl->abort_flag;
+  auto give_up = [&] {
+    ctl->abort_flag = 1;
+    atomicOr(a.err, kErrTimeout);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R::kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->accfull[s], 1);
+      mbar_init(&ctl->accempty[s], kEpiWarps);
+      for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ctl->res[w][s], 1);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA (one thread)
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+        const int t0 = static_cast<int>(tile / ncol) * kM, n0 = static_cast<int>(tile % ncol) * kN;
+        for (int k = 0; k < nk; ++k, ++it) {
+          const uint32_t s = it % R::kStages, ph = (it / R::kStages) & 1;
+          if (it >= R::kStages && !mbar_wait_bounded(&ctl->empty[s], ph ^ 1, lim, abortp)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->full[s], kStageBytes);
+          tma_load_2d(smem + s * kStageBytes, &a.x, &ctl->full[s], k * kChunk, t0);
+          tma_load_2d(smem + s * kStageBytes + kABytes, &a.w, &ctl->full[s], k * kChunk, n0);
+        }
+      }
+      for (uint32_t k = 0; k < R::kStages && k < it; ++k) {
+        const uint32_t last = it - 1 - k;
+        if (!mbar_wait_drain(&ctl->full[last % R::kStages], (last / R::kStages) & 1, lim)) atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA (one thread)
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(kN);
+      const uint64_t adesc = umma_desc_sw128(smem_u32(smem)), bdesc = umma_desc_sw128(smem_u32(smem) + kABytes);
+      uint32_t it = 0, acc = 0;
+      bool ok = true;
+      for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+        for (int k = 0; k < nk; ++k, ++it) {
+          const uint32_t s = it % R::kStages, ph = (it / R::kStages) & 1;
+          const uint32_t buf = acc & 1;
+          const bool fresh = k % flush == 0;
+          if (fresh && acc >= 2 && !mbar_wait_bounded(&ctl->accempty[buf], ((acc >> 1) & 1) ^ 1, lim, abortp)) ok = false;
+          if (ok && !mbar_wait_bounded(&ctl->full[s], ph, lim, abortp)) ok = false;
+          if (!ok) {
+            give_up();
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t off = static_cast<uint64_t>((s * kStageBytes + kk * 32) >> 4);
+            umma_ss_f16(tmem + buf * kN, adesc + off, bdesc + off, idesc, (!fresh || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&ctl->empty[s]);
+          if (k % flush == flush - 1 || k == nk - 1) {
+            umma_commit(&ctl->accfull[buf]);
+            ++acc;
+          }
+        }
+      }
+      if (it > 0) {
+        umma_commit(&ctl->drain);
+        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue: 32 rows x 128 columns per warp
+    const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+    uint8_t* mybuf = bufs + ew * R::kBufs * kBufBytes;
+    constexpr int kCols = F32OUT ? 32 : 64;          // columns of one 128-byte buffer row
+    constexpr int kPieces = 128 / kCols;
+    uint32_t acc = 0, piece = 0;                     // accumulators read, output pieces written
+    bool ok = true;
+    for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+      const int t0 = static_cast<int>(tile / ncol) * kM + 32 * q, n0 = static_cast<int>(tile % ncol) * kN + 128 * half;
+      const int pieces = (t0 < a.T && n0 < a.Cout) ? min(kPieces, (a.Cout - n0 + kCols - 1) / kCols) : 0;
+      // the residual of the first piece is on its way while the products run
+      if (RES && pieces > 0 && lane == 0) {
+        tma_store_wait_read<1>();
+        mbar_arrive_expect_tx(&ctl->res[ew][piece & 1], kBufBytes);
+        tma_load_2d(mybuf + (piece & 1) * kBufBytes, &a.res, &ctl->res[ew][piece & 1], n0, t0);
+      }
+      float v[128];
+      if (F32OUT) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) v[j] = 0.f;
+      }
+      for (int k0 = 0; k0 < nk; k0 += flush, ++acc) {
+        const uint32_t buf = acc & 1;
+        const bool okw = mbar_wait_bounded(&ctl->accfull[buf], (acc >> 1) & 1, lim, abortp);
+        if (!__all_sync(0xffffffffu, okw)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + 128 * half;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(src + 16 * g, r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[16 * g + j] = F32OUT ? v[16 * g + j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->accempty[buf]);
+      }
+      if (!ok) {
+        if (lane == 0) {
+          give_up();
+          // a residual load in flight lands before the CTA ends
+          if (RES && pieces > 0 && !mbar_wait_drain(&ctl->res[ew][piece & 1], (piece >> 1) & 1, lim))
+            atomicOr(a.err, kErrTimeout);
+        }
+        __syncwarp();
+        break;
+      }
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        if (p >= pieces || !ok) continue;
+        uint8_t* buf = mybuf + (RES ? (piece & 1) : 0) * kBufBytes;
+        const int c0 = n0 + p * kCols;
+        if (RES) {
+          if (p + 1 < pieces && lane == 0) {          // the next piece's residual
+            tma_store_wait_read<0>();
+            mbar_arrive_expect_tx(&ctl->res[ew][(piece + 1) & 1], kBufBytes);
+            tma_load_2d(mybuf + ((piece + 1) & 1) * kBufBytes, &a.res, &ctl->res[ew][(piece + 1) & 1], c0 + kCols, t0);
+          }
+          const bool okw = mbar_wait_bounded(&ctl->res[ew][piece & 1], (piece >> 1) & 1, lim, abortp);
+          if (!__all_sync(0xffffffffu, okw)) {
+            ok = false;
+            if (lane == 0) {
+              give_up();
+              for (uint32_t i = 0; i < 2; ++i)
+                if (!i || p + 1 < pieces)
+                  if (!mbar_wait_drain(&ctl->res[ew][(piece + i) & 1], ((piece + i) >> 1) & 1, lim))
+                    atomicOr(a.err, kErrTimeout);
+            }
+            __syncwarp();
+            continue;
+          }
+        } else {
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+        }
+        const uint32_t row = smem_u32(buf) + lane * 128u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {                 // 16-byte vectors of the 128-byte row
+          constexpr int kE = F32OUT ? 4 : 8;
+          const uint32_t at = row + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4);
+          const int c = c0 + j * kE;
+          float y[kE];
+#pragma unroll
+          for (int e = 0; e < kE; ++e) y[e] = v[p * kCols + j * kE + e];
+          if (c < a.Cout) {                           // Cout is a multiple of 8: a vector is in or out
+#pragma unroll
+            for (int e = 0; e < kE; e += 4) {
+              const float4 b = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              y[e] += b.x;
+              y[e + 1] += b.y;
+              y[e + 2] += b.z;
+              y[e + 3] += b.w;
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) y[e] = activate(y[e], a.act);
+            if (a.scale) {
+#pragma unroll
+              for (int e = 0; e < kE; e += 4) {
+                const float4 b = __ldg(reinterpret_cast<const float4*>(a.scale + c + e));
+                y[e] *= b.x;
+                y[e + 1] *= b.y;
+                y[e + 2] *= b.z;
+                y[e + 3] *= b.w;
+              }
+            }
+          }
+          uint32_t o[4];
+          if (RES) {
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(at) : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (F32OUT) {
+                y[e] += __uint_as_float(o[e]);
+              } else {
+                y[2 * e % kE] += bf16_lo(o[e]);
+                y[(2 * e + 1) % kE] += bf16_hi(o[e]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = F32OUT ? __float_as_uint(y[e]) : pack_bf16x2(y[2 * e % kE], y[(2 * e + 1) % kE]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                       ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(buf, &a.out, c0, t0);
+          tma_store_commit();
+        }
+        ++piece;
+      }
+    }
+    if (lane == 0) tma_store_wait<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+constexpr int kSplitThreads = 256, kSplitStages = 6;
+constexpr int kWBytes = 128 * 128;                 // a stage's weights: 128 columns x 64 channels
+
+struct SplitArgs {
+  CUtensorMap x, w;
+  const float* bias;
+  const float* scale;
+  const void* residual;
+  void* out;
+  long long residual_stride, out_stride;
+  int T, Cin, Cout, act;
+  int nparts;                // accumulators side by side (fp32 outputs: at most 512 channels each, where they fit)
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+
+struct SplitCtl {
+  uint64_t full[kSplitStages], empty[kSplitStages], accfull, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int N>
+constexpr size_t split_smem() {
+  return 1024 + kSplitStages * static_cast<size_t>(kWBytes + N * 128) + sizeof(SplitCtl);
+}
+
+template <int N, typename TO>
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_constant__ SplitArgs a, int S) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kBytes = kWBytes + N * 128;
+  static_assert(N * 512 <= kSplitStages * kBytes, "the partial sums take the ring's place");
+  SplitCtl* ctl = reinterpret_cast<SplitCtl*>(smem + kSplitStages * kBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S;                   // = the rank in the cluster
+  const int n0 = (blockIdx.x / S) * 128, t0 = blockIdx.y * N;
+  const int nkall = (a.Cin + kChunk - 1) / kChunk;
+  const int kb = static_cast<int>(static_cast<long long>(nkall) * rank / S);
+  const int nk = static_cast<int>(static_cast<long long>(nkall) * (rank + 1) / S) - kb;   // may be 0
+  const int per = max(1, (nk + a.nparts - 1) / a.nparts);            // stages per accumulator
+  const int parts = (nk + per - 1) / per;
+  const uint32_t ncols = a.nparts * N < 32 ? 32u : static_cast<uint32_t>(a.nparts * N);   // nparts: a power of 2
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abortp = &ctl->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSplitStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    mbar_init(&ctl->accfull, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, ncols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (; it < static_cast<uint32_t>(nk); ++it) {
+        const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
+        if (it >= kSplitStages && !mbar_wait_bounded(&ctl->empty[s], ph ^ 1, lim, abortp)) {
+          ctl->abort_flag = 1;
+          atomicOr(a.err, kErrTimeout);
+          break;
+        }
+        mbar_arrive_expect_tx(&ctl->full[s], kBytes);
+        tma_load_2d(smem + s * kBytes, &a.w, &ctl->full[s], (kb + static_cast<int>(it)) * kChunk, n0);
+        tma_load_2d(smem + s * kBytes + kWBytes, &a.x, &ctl->full[s], (kb + static_cast<int>(it)) * kChunk, t0);
+      }
+      for (uint32_t k = 0; k < kSplitStages && k < it; ++k) {
+        const uint32_t last = it - 1 - k;
+        if (!mbar_wait_drain(&ctl->full[last % kSplitStages], (last / kSplitStages) & 1, lim)) atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(N);
+      const uint64_t wdesc = umma_desc_sw128(smem_u32(smem)), xdesc = umma_desc_sw128(smem_u32(smem) + kWBytes);
+      bool ok = true;
+      uint32_t it = 0;
+      for (; it < static_cast<uint32_t>(nk); ++it) {
+        const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
+        if (!mbar_wait_bounded(&ctl->full[s], ph, lim, abortp)) {
+          ctl->abort_flag = 1;
+          atomicOr(a.err, kErrTimeout);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((s * kBytes + kk * 32) >> 4);
+          umma_ss_f16(tmem + (it / per) * N, wdesc + off, xdesc + off, idesc, (it % per || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(&ctl->empty[s]);
+      }
+      if (ok) umma_commit(&ctl->accfull);
+      if (it > 0) {
+        umma_commit(&ctl->drain);
+        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  }
+  // a CTA's own partial sums, [N rows][128 columns] fp32, over the ring (no product reads it any more)
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp >= 4) {
+    const int q = warp & 3;
+    const bool okw = mbar_wait_bounded(&ctl->accfull, 0, lim, abortp);
+    if (__all_sync(0xffffffffu, okw)) {
+      tc_fence_after();
+      const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+      for (int g = 0; g < N / 16; ++g) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        for (int p = 0; p < parts; ++p) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(src + p * N + 16 * g, r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(16 * g + j) * 128 + 32 * q + lane] = v[j];
+      }
+    } else if (lane == 0) {
+      ctl->abort_flag = 1;
+      atomicOr(a.err, kErrTimeout);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  // tensor memory is given back before any wait for another CTA, so that no CTA
+  // holds it while it waits
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, ncols);
+  }
+  if (S > 1) cluster_sync();
+  const uint32_t base = smem_u32(part);
+  const int c = n0 + 4 * lane;
+  if (c < a.Cout) {
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f), sc = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (a.bias) b = *reinterpret_cast<const float4*>(a.bias + c);
+    if (a.scale) sc = *reinterpret_cast<const float4*>(a.scale + c);
+    for (int n = rank * (N / S) + warp; n < (rank + 1) * (N / S) && t0 + n < a.T; n += kSplitThreads / 32) {
+      const long long t = t0 + n;
+      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.residual) res = load4(static_cast<const TO*>(a.residual) + t * a.residual_stride + c);
+      float4 y = b;
+      const uint32_t at = base + (n * 128 + 4 * lane) * 4;
+      for (int s = 0; s < S; ++s) {
+        const float4 v = S > 1 ? cluster_load4(cluster_map(at, s)) : *reinterpret_cast<const float4*>(part + n * 128 + 4 * lane);
+        y.x += v.x;
+        y.y += v.y;
+        y.z += v.z;
+        y.w += v.w;
+      }
+      y.x = fmaf(sc.x, activate(y.x, a.act), res.x);
+      y.y = fmaf(sc.y, activate(y.y, a.act), res.y);
+      y.z = fmaf(sc.z, activate(y.z, a.act), res.z);
+      y.w = fmaf(sc.w, activate(y.w, a.act), res.w);
+      store4(static_cast<TO*>(a.out) + t * a.out_stride + c, y);
+    }
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync();                         // nobody leaves while its shared memory is read
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+bool encode(CUtensorMap* m, bool bf16, const void* base, long long cols, long long rows, long long stride, int box_cols,
+            int box_rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                    const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool F32OUT, bool RES>
+cudaError_t go_rows(const RowsArgs& r, unsigned grid, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(rows_kernel<F32OUT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(Ring<RES>::kSmem));
+  if (e != cudaSuccess) return e;
+  rows_kernel<F32OUT, RES><<<grid, kThreads, Ring<RES>::kSmem, stream>>>(r);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
+  RowsArgs r{};
+  const int cols = a.out_bf16 ? 64 : 32;
+  if (!encode(&r.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, kM) ||
+      !encode(&r.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, kN) ||
+      !encode(&r.out, a.out_bf16, a.out, a.Cout, a.T, a.out_stride, cols, 32) ||
+      (a.residual && !encode(&r.res, a.out_bf16, a.residual, a.Cout, a.T, a.residual_stride, cols, 32))) {
+    *why = "tensor map encoding failed";
+    return cudaErrorInvalidValue;
+  }
+  r.bias = a.bias;
+  r.scale = a.scale;
+  r.T = a.T;
+  r.Cin = a.Cin;
+  r.Cout = a.Cout;
+  r.act = a.act;
+  r.err = a.err;
+  r.wait_limit_ns = a.wait_limit_ns;
+  const long long tiles = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + kN - 1) / kN);
+  const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
+  if (a.out_bf16) return a.residual ? go_rows<false, true>(r, grid, stream) : go_rows<false, false>(r, grid, stream);
+  return a.residual ? go_rows<true, true>(r, grid, stream) : go_rows<true, false>(r, grid, stream);
+}
+
+template <int N, typename TO>
+cudaError_t go_split(const SplitArgs& p, int S, unsigned ctiles, unsigned rtiles, cudaStream_t stream) {
+  constexpr size_t bytes = split_smem<N>();
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<N, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctiles * S, rtiles);
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, split_kernel<N, TO>, p, S);
+}
+
+template <int N>
+cudaError_t launch_split(const LinearArgs& a, int S, cudaStream_t stream, const char** why) {
+  SplitArgs p{};
+  if (!encode(&p.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, N) ||
+      !encode(&p.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, 128)) {
+    *why = "tensor map encoding failed";
+    return cudaErrorInvalidValue;
+  }
+  p.bias = a.bias;
+  p.scale = a.scale;
+  p.residual = a.residual;
+  p.out = a.out;
+  p.residual_stride = a.residual_stride;
+  p.out_stride = a.out_stride;
+  p.T = a.T;
+  p.Cin = a.Cin;
+  p.Cout = a.Cout;
+  p.act = a.act;
+  p.err = a.err;
+  p.wait_limit_ns = a.wait_limit_ns;
+  p.nparts = 1;
+  const int per_cta = ((a.Cin + kChunk - 1) / kChunk + S - 1) / S;
+  if (!a.out_bf16)
+    while (p.nparts * kFlush < per_cta && 2 * p.nparts * N <= 512) p.nparts *= 2;
+  const unsigned ctiles = (a.Cout + 127) / 128, rtiles = (static_cast<unsigned>(a.T) + N - 1) / N;
+  return a.out_bf16 ? go_split<N, __nv_bfloat16>(p, S, ctiles, rtiles, stream)
+                    : go_split<N, float>(p, S, ctiles, rtiles, stream);
+}
+
+}  // namespace lintc
+
+cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
+  using namespace lintc;
+  const long long big = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + kN - 1) / kN);
+  if (big > num_sms / 2) return launch_rows(a, num_sms, stream, why);
+  const int N = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  const long long tiles = (static_cast<long long>(a.T) + N - 1) / N * ((a.Cout + 127) / 128);
+  const int nk = (a.Cin + kChunk - 1) / kChunk;
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= num_sms && nk >= 4 * S) S *= 2;
+  switch (N) {
+    case 16:
+      return launch_split<16>(a, S, stream, why);
+    case 32:
+      return launch_split<32>(a, S, stream, why);
+    case 64:
+      return launch_split<64>(a, S, stream, why);
+    default:
+      return launch_split<128>(a, S, stream, why);
+  }
+}
+
+}  // namespace gkd
