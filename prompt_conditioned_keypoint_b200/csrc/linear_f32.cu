@@ -49,7 +49,11 @@ __global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ Lin
     float y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      y[j] = activate(acc[i][j] + (a.bias ? a.bias[n + j] : 0.f), a.act);
+      y[j] = acc[i][j] + (a.bias ? a.bias[n + j] : 0.f);
+    }
+    activate(y, a.act);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       if (a.scale) y[j] *= a.scale[n + j];
       y[j] += rv[j];
     }

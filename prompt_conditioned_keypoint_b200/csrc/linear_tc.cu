@@ -264,8 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
               y[e + 2] += b.z;
               y[e + 3] += b.w;
             }
-#pragma unroll
-            for (int e = 0; e < kE; ++e) y[e] = activate(y[e], a.act);
+            activate(y, a.act);
             if (a.scale) {
 #pragma unroll
               for (int e = 0; e < kE; e += 4) {
@@ -490,11 +489,11 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
         y.z += v.z;
         y.w += v.w;
       }
-      y.x = fmaf(sc.x, activate(y.x, a.act), res.x);
-      y.y = fmaf(sc.y, activate(y.y, a.act), res.y);
-      y.z = fmaf(sc.z, activate(y.z, a.act), res.z);
-      y.w = fmaf(sc.w, activate(y.w, a.act), res.w);
-      store4(static_cast<TO*>(a.out) + t * a.out_stride + c, y);
+      float z[4] = {y.x, y.y, y.z, y.w};
+      activate(z, a.act);
+      store4(static_cast<TO*>(a.out) + t * a.out_stride + c,
+             make_float4(fmaf(sc.x, z[0], res.x), fmaf(sc.y, z[1], res.y), fmaf(sc.z, z[2], res.z),
+                         fmaf(sc.w, z[3], res.w)));
     }
   }
   __syncwarp();
