@@ -756,7 +756,9 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
   const char* why = "";
-  const cudaError_t e = gkd::launch_attention(a, dt == GKD_BF16, static_cast<cudaStream_t>(stream), &why);
+  const cudaError_t e = dt == GKD_BF16
+                            ? gkd::launch_attention_tc(a, ds->num_sms, static_cast<cudaStream_t>(stream), &why)
+                            : gkd::launch_attention_f32(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "attention: %s", why);
   return launched(e, "attention");
 }

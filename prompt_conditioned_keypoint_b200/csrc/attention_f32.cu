@@ -1,4 +1,4 @@
-// gkd_attention on the fp32 units: out = softmax(scale q k^T) v under a key mask.
+// gkd_attention on the fp32 units, fp32: out = softmax(scale q k^T) v under a key mask.
 //
 // One CTA per (batch, head, 64 query rows). Keys come 64 at a time: a thread has
 // 4 rows x 8 keys of the scores and 4 rows x (D / 8) columns of the output, with
@@ -15,8 +15,8 @@ namespace att {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 128;
 
-template <typename T, int DC>   // DC: head columns in units of 32, rounded up
-__global__ void __launch_bounds__(kThreads) attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
+template <int DC>   // DC: head columns in units of 32, rounded up
+__global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_constant__ AttentionArgs a) {
   extern __shared__ float sm[];
   constexpr int DP = 32 * DC + 4;
   float* qs = sm;
@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const __grid_c
   const int bh = blockIdx.x / ntiles, h = bh % a.q.heads, b = bh / a.q.heads;
   const int hk = h / (a.q.heads / a.k.heads);
   const int r0 = tile * kRows;
-  const T* q = static_cast<const T*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
-  const T* k = static_cast<const T*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
-  const T* v = static_cast<const T*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
-  T* o = static_cast<T*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride;
+  const float* q = static_cast<const float*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
+  const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
+  const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
+  float* o = static_cast<float*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride;
   const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
   const int nq4 = a.D / 4;
   const float qscale = a.scale * 1.4426950408889634f;
@@ -158,38 +158,31 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const __grid_c
   }
 }
 
-template <typename T, int DC>
+template <int DC>
 cudaError_t go(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
   constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * 68);
-  cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attention_f32_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  attention_simt_kernel<T, DC><<<grid, kThreads, bytes, stream>>>(a);
+  attention_f32_kernel<DC><<<grid, kThreads, bytes, stream>>>(a);
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t pick(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
-  switch ((a.D + 31) / 32) {
-    case 1:
-      return go<T, 1>(a, grid, stream);
-    case 2:
-      return go<T, 2>(a, grid, stream);
-    case 3:
-      return go<T, 3>(a, grid, stream);
-    default:
-      return go<T, 4>(a, grid, stream);
-  }
 }
 
 }  // namespace att
 
-cudaError_t launch_attention(AttentionArgs& a, bool bf16, cudaStream_t stream, const char** why) {
-  (void)why;
+cudaError_t launch_attention_f32(const AttentionArgs& a, cudaStream_t stream) {
   const long long ntiles = (static_cast<long long>(a.Tq) + att::kRows - 1) / att::kRows;
-  const long long grid = ntiles * a.q.heads * a.B;
-  return bf16 ? att::pick<__nv_bfloat16>(a, static_cast<unsigned>(grid), stream)
-              : att::pick<float>(a, static_cast<unsigned>(grid), stream);
+  const unsigned grid = static_cast<unsigned>(ntiles * a.q.heads * a.B);
+  switch ((a.D + 31) / 32) {
+    case 1:
+      return att::go<1>(a, grid, stream);
+    case 2:
+      return att::go<2>(a, grid, stream);
+    case 3:
+      return att::go<3>(a, grid, stream);
+    default:
+      return att::go<4>(a, grid, stream);
+  }
 }
 
 }  // namespace gkd

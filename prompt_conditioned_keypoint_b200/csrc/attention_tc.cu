@@ -1,0 +1,576 @@
+// gkd_attention on the tensor cores, bf16: out = softmax(scale q k^T) v under a
+// key mask, one pass over the keys with a running maximum and sum.
+//
+// A CTA has 128 query rows of one head (a row per tensor-memory lane) and walks
+// over tiles of BN keys: S = Q K^T into tensor memory (fp32), p = 2^(s - m) by one
+// thread per row, P back into tensor memory as bf16, O += P V with P as the
+// tensor-memory operand and V as a shared-memory operand read across its rows
+// (head columns contiguous). Two CTAs share an SM (half of its tensor memory
+// and of its shared memory each), so that one's products run under the other's
+// exponentials.
+//
+//   warp 0     decides which key tiles are worth doing (mask and diagonal), hands
+//              their key bits to the others through a small ring, and loads Q, K
+//              and V by TMA (128B-swizzled, zeros past every edge);
+//   warp 1     issues the products: S of the next tile ahead of O of this one;
+//   warps 2-5  softmax: scores are read twice from tensor memory (maximum, then
+//              weights). O is rescaled only when a row's maximum has grown by
+//              more than 2^8 since the last time; until then the weights are
+//              taken against the older maximum, which changes nothing but their
+//              common scale (they stay below 2^8).
+//
+// Hidden keys: their scores are replaced by -inf, and their rows of V in shared
+// memory are zeroed before the product (0 x NaN would be NaN).
+// Few query tiles: a cluster of S CTAs shares the key tiles of one query tile and
+// joins (O, m, l) through shared memory in rank order.
+// The weights are rounded to bf16 for the second product (the operand type); their
+// sum l is taken from the fp32 values.
+#include "blocks_common.cuh"
+#include "gkd_internal.h"
+
+namespace gkd {
+namespace atc {
+
+constexpr int kThreads = 192, kRows = 128, kKvStages = 2, kInfo = 4;
+constexpr int kKvBytes = 16384;                     // a stage of K (or V): 128 keys x 64 columns or 64 x 128
+constexpr float kGrow = 8.f;                        // rescale O when a maximum grew by more than this (log2)
+
+struct Args {
+  CUtensorMap q, k, v;                              // {D, rows, heads, batch}
+  void* out;
+  long long out_bs, out_rs, out_hs;
+  int heads, group;                                 // query heads, query heads per key head
+  int kb_shared;                                    // bit 0: q, 1: k, 2: v has one batch for all
+  int Tq, Tk, D, causal, ntiles;
+  float scale_log2;                                 // scale * log2(e)
+  const uint8_t* mask;
+  long long mask_bs;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+
+struct Info {                                       // one key tile
+  int k0;                                           // first key, or -1: no more tiles
+  int plain;                                        // every key of the tile is visible to every row of the CTA
+  uint32_t bits[4];                                 // keys that the mask and Tk leave
+};
+
+struct Ctl {
+  uint64_t qfull, kfull[kKvStages], kempty[kKvStages], vfull[kKvStages], vempty[kKvStages];
+  uint64_t ifull[kInfo], iempty[kInfo], sfull, pready, pvdone, drain;
+  Info info[kInfo];
+  uint32_t tmem_base;
+  int abort_flag;
+  float m[kRows], l[kRows];                         // of the rows, for the other CTAs of the cluster
+};
+
+// Descriptor of V for the second product: the 64-column chunk of a key row is contiguous
+// (MN-major, 128B swizzle); 8 key rows to 1024 bytes (SBO), chunks `lbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t lbo) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+template <int DCH>
+__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_constant__ Args a, int S) {
+  constexpr int BN = DCH == 1 ? 128 : 64, W = BN / 32;               // keys per tile, words of key bits
+  constexpr uint32_t kColP = BN, kColO = DCH == 1 ? 192 : 128;       // S at column 0
+  constexpr int kQBytes = kRows * 128 * DCH;
+  static_assert(BN * 128 * DCH == kKvBytes, "stage");
+  static_assert(kRows * DCH * 64 * 4 <= 2 * kKvStages * kKvBytes, "the partial output takes the ring's place");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ks = smem + kQBytes;
+  uint8_t* vs = ks + kKvStages * kKvBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(vs + kKvStages * kKvBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S;
+  const int work = blockIdx.x / S;
+  const int tile = a.ntiles - 1 - work % a.ntiles;  // with a diagonal the last rows have the most keys: first
+  const int bh = work / a.ntiles, h = bh % a.heads, b = bh / a.heads, hk = h / a.group;
+  const int r0 = tile * kRows;
+  const long long shift = static_cast<long long>(a.Tk) - a.Tq;       // causal: key j for row i iff j <= i + shift
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abortp = &ctl->abort_flag;
+  auto give_up = [&] {
+    ctl->abort_flag = 1;
+    atomicOr(a.err, kErrTimeout);
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->qfull, 1);
+    for (int s = 0; s < kKvStages; ++s) {
+      mbar_init(&ctl->kfull[s], 1);
+      mbar_init(&ctl->kempty[s], 1);
+      mbar_init(&ctl->vfull[s], 1);
+      mbar_init(&ctl->vempty[s], 1);
+    }
+    for (int s = 0; s < kInfo; ++s) {
+      mbar_init(&ctl->ifull[s], 1);
+      mbar_init(&ctl->iempty[s], 5);                // four softmax warps and the MMA thread
+    }
+    mbar_init(&ctl->sfull, 1);
+    mbar_init(&ctl->pready, 4);
+    mbar_init(&ctl->pvdone, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 256);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- tiles, key bits, TMA
+    long long klast = a.Tk;                         // keys that some row of this CTA may see
+    if (a.causal) klast = max(0ll, min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift));
+    const int all = static_cast<int>((klast + BN - 1) / BN);
+    const int lo = static_cast<int>(static_cast<long long>(all) * rank / S);
+    const int hi = static_cast<int>(static_cast<long long>(all) * (rank + 1) / S);
+    const uint8_t* mask = a.mask ? a.mask + b * a.mask_bs : nullptr;
+    const int bq = a.kb_shared & 1 ? 0 : b, bk = a.kb_shared & 2 ? 0 : b, bv = a.kb_shared & 4 ? 0 : b;
+    uint32_t n = 0;                                 // tiles handed on
+    bool ok = true;
+    uint8_t next[W];                                // mask bytes of the coming tile, loaded ahead
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const long long key = static_cast<long long>(t) * BN + 32 * w + lane;
+        next[w] = t < hi && key < a.Tk && mask ? mask[key] : 0;
+      }
+    };
+    if (mask) fetch(lo);
+    for (int t = lo; t <= hi && ok; ++t) {
+      const bool end = t == hi;
+      const int k0 = t * BN;
+      uint32_t bits[W], any = 0, every = 0xffffffffu;
+      if (!end) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const bool live = k0 + 32 * w + lane < a.Tk && (!mask || next[w] != 0);
+          bits[w] = __ballot_sync(0xffffffffu, live);
+          any |= bits[w];
+          every &= bits[w];
+        }
+        if (mask) fetch(t + 1);
+        if (!any) continue;
+      }
+      const uint32_t is = n % kInfo;
+      if (n >= kInfo) {
+        const bool okw = mbar_wait_bounded(&ctl->iempty[is], ((n / kInfo) & 1) ^ 1, lim, abortp);
+        if (!__all_sync(0xffffffffu, okw)) ok = false;
+      }
+      if (ok && lane == 0) {
+        Info& f = ctl->info[is];
+        f.k0 = end ? -1 : k0;
+        if (!end) {
+          f.plain = every == 0xffffffffu && (!a.causal || k0 + BN - 1 <= r0 + shift);
+#pragma unroll
+          for (int w = 0; w < W; ++w) f.bits[w] = bits[w];
+        }
+        mbar_arrive(&ctl->ifull[is]);
+      }
+      __syncwarp();
+      if (end || !ok) break;
+      if (lane == 0) {
+        if (n == 0) {
+          mbar_arrive_expect_tx(&ctl->qfull, kQBytes);
+          for (int c = 0; c < DCH; ++c)
+            tma_load_4d(smem + c * kRows * 128, &a.q, &ctl->qfull, 64 * c, r0, h, bq);
+        }
+        const uint32_t s = n % kKvStages, ph = (n / kKvStages) & 1;
+        if (n < kKvStages || mbar_wait_bounded(&ctl->kempty[s], ph ^ 1, lim, abortp)) {
+          mbar_arrive_expect_tx(&ctl->kfull[s], kKvBytes);
+          for (int c = 0; c < DCH; ++c)
+            tma_load_4d(ks + s * kKvBytes + c * BN * 128, &a.k, &ctl->kfull[s], 64 * c, k0, hk, bk);
+          if (n < kKvStages || mbar_wait_bounded(&ctl->vempty[s], ph ^ 1, lim, abortp)) {
+            mbar_arrive_expect_tx(&ctl->vfull[s], kKvBytes);
+            for (int c = 0; c < DCH; ++c)
+              tma_load_4d(vs + s * kKvBytes + c * BN * 128, &a.v, &ctl->vfull[s], 64 * c, k0, hk, bv);
+          } else {
+            if (!mbar_wait_drain(&ctl->kfull[s], ph, lim)) atomicOr(a.err, kErrTimeout);
+            ok = false;
+          }
+        } else {
+          ok = false;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok) ++n;
+    }
+    if (lane == 0) {
+      if (!ok) give_up();
+      if (n > 0 && !mbar_wait_drain(&ctl->qfull, 0, lim)) atomicOr(a.err, kErrTimeout);
+      for (uint32_t i = 0; i < kKvStages && i < n; ++i) {
+        const uint32_t last = n - 1 - i, s = last % kKvStages, ph = (last / kKvStages) & 1;
+        if (!mbar_wait_drain(&ctl->kfull[s], ph, lim) || !mbar_wait_drain(&ctl->vfull[s], ph, lim))
+          atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products (one thread)
+    if (lane == 0) {
+      const int dk = (a.D + 15) / 16;                                // K = 16 steps of the first product
+      const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) | (8u << 24);
+      const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
+      const uint64_t qd = umma_desc_sw128(smem_u32(smem)), kd = umma_desc_sw128(smem_u32(ks));
+      const uint64_t vd = desc_mn_sw128(smem_u32(vs), BN * 128);
+      bool ok = true, issued = false;
+      auto more = [&](uint32_t j) {                                  // is there a tile j? (its info slot is then done with)
+        const uint32_t is = j % kInfo;
+        if (!mbar_wait_bounded(&ctl->ifull[is], (j / kInfo) & 1, lim, abortp)) {
+          ok = false;
+          return false;
+        }
+        const bool is_tile = ctl->info[is].k0 >= 0;
+        mbar_arrive(&ctl->iempty[is]);
+        return is_tile;
+      };
+      auto scores = [&](uint32_t j) {
+        const uint32_t s = j % kKvStages;
+        if ((j == 0 && !mbar_wait_bounded(&ctl->qfull, 0, lim, abortp)) ||
+            !mbar_wait_bounded(&ctl->kfull[s], (j / kKvStages) & 1, lim, abortp)) {
+          ok = false;
+          return;
+        }
+        tc_fence_after();
+        for (int kk = 0; kk < dk; ++kk) {                            // four 32-byte steps per 64-column chunk
+          const uint32_t c = kk >> 2, o = (kk & 3) * 32;
+          umma_ss_f16(tmem, qd + ((c * kRows * 128 + o) >> 4), kd + ((s * kKvBytes + c * BN * 128 + o) >> 4), idesc_s,
+                      kk > 0 ? 1u : 0u);
+        }
+        issued = true;
+        umma_commit(&ctl->kempty[s]);
+        umma_commit(&ctl->sfull);
+      };
+      bool tile_ahead = more(0);
+      if (tile_ahead) scores(0);
+      for (uint32_t j = 0; tile_ahead && ok; ++j) {
+        const uint32_t s = j % kKvStages;
+        if (!mbar_wait_bounded(&ctl->pready, j & 1, lim, abortp)) {
+          ok = false;
+          break;
+        }
+        tile_ahead = more(j + 1);
+        if (tile_ahead) scores(j + 1);
+        if (!ok || !mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          umma_ts_f16(tmem + kColO, tmem + kColP + 8 * kk, vd + ((s * kKvBytes + kk * 2048) >> 4), idesc_o,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&ctl->vempty[s]);
+        umma_commit(&ctl->pvdone);
+      }
+      if (!ok) give_up();
+      if (issued) {
+        umma_commit(&ctl->drain);
+        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax: one row per thread
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float m = -INFINITY, l = 0.f;                   // the maximum that the weights are taken against, their sum
+    uint32_t j = 0;
+    bool ok = true;
+    for (;; ++j) {
+      const uint32_t is = j % kInfo;
+      bool okw = mbar_wait_bounded(&ctl->ifull[is], (j / kInfo) & 1, lim, abortp);
+      if (!__all_sync(0xffffffffu, okw)) {
+        ok = false;
+        break;
+      }
+      const int k0 = ctl->info[is].k0;
+      const bool plain = ctl->info[is].plain != 0;
+      uint32_t bits[W], hidden = 0;
+      if (k0 >= 0 && !plain) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) bits[w] = ctl->info[is].bits[w];
+        // the key of this thread when it zeroes a row of V
+        hidden = r < BN ? !((ctl->info[is].bits[r >> 5 & (W - 1)] >> lane) & 1u) : 0u;
+        if (a.causal) {
+          const long long vis = r0 + r + shift - k0 + 1;             // keys of the tile up to the diagonal
+          const int v = static_cast<int>(max(0ll, min(vis, static_cast<long long>(BN))));
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const int c = min(max(v - 32 * w, 0), 32);
+            bits[w] &= c == 32 ? 0xffffffffu : (1u << c) - 1u;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->iempty[is]);
+      if (k0 < 0) break;
+      okw = mbar_wait_bounded(&ctl->sfull, j & 1, lim, abortp);
+      if (!__all_sync(0xffffffffu, okw)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // the tile's maximum
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(lane_base + 32 * w, v);
+        tmem_wait_ld_regs(v);
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (plain) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], (bits[w] >> e) & 1u ? __uint_as_float(v[e]) : -INFINITY);
+        }
+        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+      }
+      // P and O are free once the last tile's second product is done
+      if (j > 0) {
+        okw = mbar_wait_bounded(&ctl->pvdone, (j - 1) & 1, lim, abortp);
+        if (!__all_sync(0xffffffffu, okw)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const bool grow = top > m && !((top - m) * a.scale_log2 <= kGrow);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = fmaxf(m, top);
+        const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+          for (int c = 0; c < (a.D + 15) / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
+            tmem_wait_ld_regs(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st_32x32b_x16(lane_base + kColO + 16 * c, v);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
+      // the weights
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t v[32], p[16];
+        tmem_ld_32x32b_x32(lane_base + 32 * w, v);
+        tmem_wait_ld_regs(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float x = __uint_as_float(v[e]);
+          if (!plain) x = (bits[w] >> e) & 1u ? x : -INFINITY;
+          x = ex2_approx(fmaf(x, a.scale_log2, -base));
+          sum[e & 3] += x;
+          v[e] = __float_as_uint(x);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        tmem_st_32x32b_x16(lane_base + kColP + 16 * w, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      if (!plain) {                                 // rows of V that no row may see
+        const uint32_t s = j % kKvStages;
+        okw = mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp);
+        if (!__all_sync(0xffffffffu, okw)) {
+          ok = false;
+          break;
+        }
+        if (hidden) {
+          for (int c = 0; c < DCH; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(vs + s * kKvBytes + c * BN * 128 + r * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->pready);
+    }
+    if (ok && j > 0) {
+      const bool okw = mbar_wait_bounded(&ctl->pvdone, (j - 1) & 1, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw);
+      tc_fence_after();
+    }
+    if (!ok && lane == 0) give_up();
+    const bool mine = ok && r0 + r < a.Tq;
+    if (S == 1) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs;
+      for (int c = 0; c < (a.D + 15) / 16; ++c) {
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0u;
+        if (ok && j > 0) {
+          tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
+          tmem_wait_ld_regs(v);
+        }
+        if (!mine) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          if (16 * c + e >= a.D) continue;
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
+          *reinterpret_cast<uint4*>(o + 16 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    } else {
+      // this CTA's share, over the K and V ring (its last reader, the last product, is done):
+      // row r's 16-byte pieces c at c ^ (r & 15), so that the 32 rows of a store spread over the banks
+      ctl->m[r] = m;
+      ctl->l[r] = l;
+      for (int c = 0; c < (a.D + 15) / 16; ++c) {
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0u;
+        if (ok && j > 0) {
+          tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
+          tmem_wait_ld_regs(v);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(ks + r * (256 * DCH) + (((4 * c + e) ^ (r & 15)) << 4)) =
+              make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // tensor memory is given back before any wait for another CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+  if (S > 1) {
+    cluster_sync();
+    const uint32_t om = smem_u32(ctl->m), ol = smem_u32(ctl->l), oo = smem_u32(ks);
+    const int pieces = a.D / 4, share = kRows / S;
+    for (int i = threadIdx.x; i < share * pieces; i += kThreads) {
+      const int r = rank * share + i / pieces, c = i % pieces;
+      if (r0 + r >= a.Tq) continue;
+      float m = -INFINITY;
+      for (int s = 0; s < S; ++s) m = fmaxf(m, cluster_load1(cluster_map(om + 4 * r, s)));
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < S; ++s) {
+        const float ms = cluster_load1(cluster_map(om + 4 * r, s));
+        if (ms == -INFINITY) continue;              // a share without a key for this row
+        const float f = ex2_approx((ms - m) * a.scale_log2);
+        const float4 v = cluster_load4(cluster_map(oo + r * (256 * DCH) + ((c ^ (r & 15)) << 4), s));
+        l = fmaf(f, cluster_load1(cluster_map(ol + 4 * r, s)), l);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store4(static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs + 4 * c,
+             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    __syncwarp();
+    cluster_sync();                                 // nobody leaves while its shared memory is read
+  }
+}
+
+// Attention over no keys: zeros.
+__global__ void __launch_bounds__(128) zero_kernel(__nv_bfloat16* out, long long bs, long long rs, long long hs, int B,
+                                                   int T, int heads, int D) {
+  for (long long row = blockIdx.x; row < static_cast<long long>(B) * T; row += gridDim.x)
+    for (int i = threadIdx.x; i < heads * (D / 8); i += blockDim.x)
+      *reinterpret_cast<uint4*>(out + row / T * bs + row % T * rs + i / (D / 8) * hs + i % (D / 8) * 8) =
+          make_uint4(0u, 0u, 0u, 0u);
+}
+
+bool encode(CUtensorMap* m, const HeadsView& t, int B, int rows, int D, int box_rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(t.heads),
+                              static_cast<cuuint64_t>(t.batch_stride ? B : 1)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t.row_stride) * 2, static_cast<cuuint64_t>(t.head_stride) * 2,
+                                 static_cast<cuuint64_t>(t.batch_stride ? t.batch_stride : t.row_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.data, dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DCH>
+cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
+  constexpr size_t bytes = 1024 + kRows * 128 * DCH + 2 * kKvStages * kKvBytes + sizeof(Ctl);
+  static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DCH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(work * S);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_kernel<DCH>, a, S);
+}
+
+}  // namespace atc
+
+cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t stream, const char** why) {
+  using namespace atc;
+  if (a.Tk == 0) {
+    const long long rows = static_cast<long long>(a.B) * a.Tq;
+    zero_kernel<<<static_cast<unsigned>(rows < 65536 ? rows : 65536), 128, 0, stream>>>(
+        static_cast<__nv_bfloat16*>(a.out.data), a.out.batch_stride, a.out.row_stride, a.out.head_stride, a.B, a.Tq,
+        a.q.heads, a.D);
+    return cudaGetLastError();
+  }
+  Args p{};
+  const int bn = a.D <= 64 ? 128 : 64;
+  if (!encode(&p.q, a.q, a.B, a.Tq, a.D, kRows) || !encode(&p.k, a.k, a.B, a.Tk, a.D, bn) ||
+      !encode(&p.v, a.v, a.B, a.Tk, a.D, bn)) {
+    *why = "tensor map encoding failed";
+    return cudaErrorInvalidValue;
+  }
+  p.out = a.out.data;
+  p.out_bs = a.out.batch_stride;
+  p.out_rs = a.out.row_stride;
+  p.out_hs = a.out.head_stride;
+  p.heads = a.q.heads;
+  p.group = a.q.heads / a.k.heads;
+  p.kb_shared = (a.q.batch_stride ? 0 : 1) | (a.k.batch_stride ? 0 : 2) | (a.v.batch_stride ? 0 : 4);
+  p.Tq = a.Tq;
+  p.Tk = a.Tk;
+  p.D = a.D;
+  p.causal = a.causal;
+  p.ntiles = static_cast<int>((static_cast<long long>(a.Tq) + kRows - 1) / kRows);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.mask = a.mask;
+  p.mask_bs = a.mask_batch_stride;
+  p.err = a.err;
+  p.wait_limit_ns = a.wait_limit_ns;
+  const long long work = static_cast<long long>(p.ntiles) * a.q.heads * a.B;
+  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + bn - 1) / bn);
+  int S = 1;
+  while (S < 8 && work * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
+  return a.D <= 64 ? go<1>(p, S, static_cast<unsigned>(work), stream) : go<2>(p, S, static_cast<unsigned>(work), stream);
+}
+
+}  // namespace gkd
