@@ -13,8 +13,8 @@
 //              their key bits to the others through a small ring, and loads Q, K
 //              and V by TMA (128B-swizzled, zeros past every edge);
 //   warp 1     issues the products: S of the next tile ahead of O of this one;
-//   warps 2-5  softmax: scores are read twice from tensor memory (maximum, then
-//              weights). O is rescaled only when a row's maximum has grown by
+//   warps 2-5  softmax: a row's scores go into registers at once, which frees their
+//              place for the next tile's product. O is rescaled only when a row's maximum has grown by
 //              more than 2^8 since the last time; until then the weights are
 //              taken against the older maximum, which changes nothing but their
 //              common scale (they stay below 2^8).
@@ -52,12 +52,13 @@ struct Args {
 struct Info {                                       // one key tile
   int k0;                                           // first key, or -1: no more tiles
   int plain;                                        // every key of the tile is visible to every row of the CTA
+  int words;                                        // 32-key groups up to the last visible key; the rest is left out
   uint32_t bits[4];                                 // keys that the mask and Tk leave
 };
 
 struct Ctl {
   uint64_t qfull, kfull[kKvStages], kempty[kKvStages], vfull[kKvStages], vempty[kKvStages];
-  uint64_t ifull[kInfo], iempty[kInfo], sfull, pready, pvdone, drain;
+  uint64_t ifull[kInfo], iempty[kInfo], sfull, sread, pready, pvdone, drain;
   Info info[kInfo];
   uint32_t tmem_base;
   int abort_flag;
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
       mbar_init(&ctl->iempty[s], 5);                // four softmax warps and the MMA thread
     }
     mbar_init(&ctl->sfull, 1);
+    mbar_init(&ctl->sread, 4);
     mbar_init(&ctl->pready, 4);
     mbar_init(&ctl->pvdone, 1);
     mbar_init(&ctl->drain, 1);
@@ -169,8 +171,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
         f.k0 = end ? -1 : k0;
         if (!end) {
           f.plain = every == 0xffffffffu && (!a.causal || k0 + BN - 1 <= r0 + shift);
+          f.words = 1;
 #pragma unroll
-          for (int w = 0; w < W; ++w) f.bits[w] = bits[w];
+          for (int w = 0; w < W; ++w) {
+            f.bits[w] = bits[w];
+            if (bits[w]) f.words = w + 1;
+          }
         }
         mbar_arrive(&ctl->ifull[is]);
       }
@@ -216,22 +222,22 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
     // ---------------------------------------------------------------- products (one thread)
     if (lane == 0) {
       const int dk = (a.D + 15) / 16;                                // K = 16 steps of the first product
-      const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) | (8u << 24);
+      const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);      // and N = the keys taken
       const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
       const uint64_t qd = umma_desc_sw128(smem_u32(smem)), kd = umma_desc_sw128(smem_u32(ks));
       const uint64_t vd = desc_mn_sw128(smem_u32(vs), BN * 128);
       bool ok = true, issued = false;
-      auto more = [&](uint32_t j) {                                  // is there a tile j? (its info slot is then done with)
+      auto more = [&](uint32_t j) {                                  // words of tile j, 0: no more (its info slot is then done with)
         const uint32_t is = j % kInfo;
         if (!mbar_wait_bounded(&ctl->ifull[is], (j / kInfo) & 1, lim, abortp)) {
           ok = false;
-          return false;
+          return 0;
         }
-        const bool is_tile = ctl->info[is].k0 >= 0;
+        const int words = ctl->info[is].k0 >= 0 ? ctl->info[is].words : 0;
         mbar_arrive(&ctl->iempty[is]);
-        return is_tile;
+        return words;
       };
-      auto scores = [&](uint32_t j) {
+      auto scores = [&](uint32_t j, int words) {
         const uint32_t s = j % kKvStages;
         if ((j == 0 && !mbar_wait_bounded(&ctl->qfull, 0, lim, abortp)) ||
             !mbar_wait_bounded(&ctl->kfull[s], (j / kKvStages) & 1, lim, abortp)) {
@@ -241,34 +247,34 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
         tc_fence_after();
         for (int kk = 0; kk < dk; ++kk) {                            // four 32-byte steps per 64-column chunk
           const uint32_t c = kk >> 2, o = (kk & 3) * 32;
-          umma_ss_f16(tmem, qd + ((c * kRows * 128 + o) >> 4), kd + ((s * kKvBytes + c * BN * 128 + o) >> 4), idesc_s,
-                      kk > 0 ? 1u : 0u);
+          umma_ss_f16(tmem, qd + ((c * kRows * 128 + o) >> 4), kd + ((s * kKvBytes + c * BN * 128 + o) >> 4),
+                      idesc_s | (static_cast<uint32_t>(words * 4) << 17), kk > 0 ? 1u : 0u);
         }
         issued = true;
         umma_commit(&ctl->kempty[s]);
         umma_commit(&ctl->sfull);
       };
-      bool tile_ahead = more(0);
-      if (tile_ahead) scores(0);
-      for (uint32_t j = 0; tile_ahead && ok; ++j) {
+      int words = more(0);
+      if (words) scores(0, words);
+      for (uint32_t j = 0; words && ok; ++j) {
         const uint32_t s = j % kKvStages;
-        if (!mbar_wait_bounded(&ctl->pready, j & 1, lim, abortp)) {
-          ok = false;
-          break;
+        const int ahead = more(j + 1);
+        if (ahead) {                                                 // once tile j's scores are in registers
+          if (!mbar_wait_bounded(&ctl->sread, j & 1, lim, abortp)) ok = false;
+          if (ok) scores(j + 1, ahead);
         }
-        tile_ahead = more(j + 1);
-        if (tile_ahead) scores(j + 1);
-        if (!ok || !mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp)) {
+        if (!ok || !mbar_wait_bounded(&ctl->pready, j & 1, lim, abortp) ||
+            !mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp)) {
           ok = false;
           break;
         }
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
+        for (int kk = 0; kk < 2 * words; ++kk)
           umma_ts_f16(tmem + kColO, tmem + kColP + 8 * kk, vd + ((s * kKvBytes + kk * 2048) >> 4), idesc_o,
                       (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&ctl->vempty[s]);
         umma_commit(&ctl->pvdone);
+        words = ahead;
       }
       if (!ok) give_up();
       if (issued) {
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
       }
       const int k0 = ctl->info[is].k0;
       const bool plain = ctl->info[is].plain != 0;
+      const int words = ctl->info[is].words;
       uint32_t bits[W], hidden = 0;
       if (k0 >= 0 && !plain) {
 #pragma unroll
@@ -318,23 +325,26 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
         break;
       }
       tc_fence_after();
-      // the tile's maximum
-      float top = -INFINITY;
+      // the tile's scores, into registers: the next tile's may then take their place
+      float x[BN];
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + 32 * w, v);
-        tmem_wait_ld_regs(v);
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (plain) {
+      for (int w = 0; w < W; ++w)
+        if (w < words) tmem_ld_32x32b_x32(lane_base + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], __uint_as_float(v[e]));
-        } else {
+      for (int w = 0; w < W; ++w) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sread);
+      if (!plain) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) t4[e & 3] = fmaxf(t4[e & 3], (bits[w] >> e) & 1u ? __uint_as_float(v[e]) : -INFINITY);
-        }
-        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[32 * w + e] = (bits[w] >> e) & 1u ? x[32 * w + e] : -INFINITY;
       }
+      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < BN; ++e) t4[e & 3] = fmaxf(t4[e & 3], x[e]);
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       // P and O are free once the last tile's second product is done
       if (j > 0) {
         okw = mbar_wait_bounded(&ctl->pvdone, (j - 1) & 1, lim, abortp);
@@ -366,19 +376,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        uint32_t v[32], p[16];
-        tmem_ld_32x32b_x32(lane_base + 32 * w, v);
-        tmem_wait_ld_regs(v);
+        if (w >= words) continue;
+        uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          float x = __uint_as_float(v[e]);
-          if (!plain) x = (bits[w] >> e) & 1u ? x : -INFINITY;
-          x = ex2_approx(fmaf(x, a.scale_log2, -base));
-          sum[e & 3] += x;
-          v[e] = __float_as_uint(x);
+          x[32 * w + e] = ex2_approx(fmaf(x[32 * w + e], a.scale_log2, -base));
+          sum[e & 3] += x[32 * w + e];
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(x[32 * w + 2 * e], x[32 * w + 2 * e + 1]);
         tmem_st_32x32b_x16(lane_base + kColP + 16 * w, p);
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
