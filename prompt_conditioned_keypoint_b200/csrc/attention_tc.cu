@@ -2,20 +2,23 @@
 // key mask, one pass over the keys with a running maximum and sum.
 //
 // A CTA has 128 query rows of one head (a row per tensor-memory lane) and walks
-// over tiles of BN keys: S = Q K^T into tensor memory (fp32), p = 2^(s - m) by one
-// thread per row, P back into tensor memory as bf16, O += P V with P as the
+// over tiles of 64 keys: S = Q K^T into tensor memory (fp32), p = 2^(s - m) by one
+// thread per row, P as bf16 over the scores it came from, O += P V with P as the
 // tensor-memory operand and V as a shared-memory operand read across its rows
-// (head columns contiguous). Two CTAs share an SM (half of its tensor memory
-// and of its shared memory each), so that one's products run under the other's
-// exponentials.
+// (head columns contiguous).
 //
-//   warp 0     decides which key tiles are worth doing (mask and diagonal), hands
-//              their key bits to the others through a small ring, and loads Q, K
-//              and V by TMA (128B-swizzled, zeros past every edge);
-//   warp 1     issues the products: S of the next tile ahead of O of this one;
-//   warps 2-5  softmax: a row's scores go into registers at once, which frees their
-//              place for the next tile's product. O is rescaled only when a row's maximum has grown by
-//              more than 2^8 since the last time; until then the weights are
+// A tile is a chain of steps that wait for one another (product, scores to
+// registers, exponentials, weights back, product), so what fills an SM is other
+// chains: heads of up to 64 columns take 128 columns of tensor memory and four
+// CTAs share an SM; wider heads take 256 with two buffers of scores (the next
+// tile's product runs under this tile's exponentials) and two CTAs share it.
+//
+//   warp 0     loads Q, K and V by TMA (128B-swizzled, zeros past every edge). With a
+//              mask it decides which key tiles are worth doing and hands their key
+//              bits to the others through a small ring;
+//   warp 1     issues the products;
+//   warps 2-5  softmax, one row per thread. O is rescaled only when a row's maximum has
+//              grown by more than 2^8 since the last time; until then the weights are
 //              taken against the older maximum, which changes nothing but their
 //              common scale (they stay below 2^8).
 //
@@ -31,8 +34,8 @@
 namespace gkd {
 namespace atc {
 
-constexpr int kThreads = 192, kRows = 128, kKvStages = 2, kInfo = 4;
-constexpr int kKvBytes = 16384;                     // a stage of K (or V): 128 keys x 64 columns or 64 x 128
+constexpr int kSoftWarps = 4, kThreads = 32 * (2 + kSoftWarps), kRows = 128, kKvStages = 2, kInfo = 4;
+constexpr int BN = 64, W = BN / 32;                 // keys per tile, words of key bits
 constexpr float kGrow = 8.f;                        // rescale O when a maximum grew by more than this (log2)
 
 struct Args {
@@ -43,7 +46,7 @@ struct Args {
   int kb_shared;                                    // bit 0: q, 1: k, 2: v has one batch for all
   int Tq, Tk, D, causal, ntiles;
   float scale_log2;                                 // scale * log2(e)
-  const uint8_t* mask;
+  const uint8_t* mask;                              // MASK kernels
   long long mask_bs;
   unsigned* err;
   unsigned long long wait_limit_ns;
@@ -53,12 +56,12 @@ struct Info {                                       // one key tile
   int k0;                                           // first key, or -1: no more tiles
   int plain;                                        // every key of the tile is visible to every row of the CTA
   int words;                                        // 32-key groups up to the last visible key; the rest is left out
-  uint32_t bits[4];                                 // keys that the mask and Tk leave
+  uint32_t bits[W];                                 // keys that the mask and Tk leave
 };
 
 struct Ctl {
   uint64_t qfull, kfull[kKvStages], kempty[kKvStages], vfull[kKvStages], vempty[kKvStages];
-  uint64_t ifull[kInfo], iempty[kInfo], sfull, sread, pready, pvdone, drain;
+  uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], pvdone, odone, drain;
   Info info[kInfo];
   uint32_t tmem_base;
   int abort_flag;
@@ -72,12 +75,11 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t l
          (1ull << 46) | (2ull << 61);
 }
 
-template <int DCH>
-__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_constant__ Args a, int S) {
-  constexpr int BN = DCH == 1 ? 128 : 64, W = BN / 32;               // keys per tile, words of key bits
-  constexpr uint32_t kColP = BN, kColO = DCH == 1 ? 192 : 128;       // S at column 0
-  constexpr int kQBytes = kRows * 128 * DCH;
-  static_assert(BN * 128 * DCH == kKvBytes, "stage");
+template <int DCH, bool MASK>
+__global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(const __grid_constant__ Args a, int S) {
+  constexpr int kBufs = DCH;                                         // buffers of scores
+  constexpr uint32_t kCols = 128 * DCH, kColO = 64 * kBufs;          // scores at 0 (and 64)
+  constexpr int kQBytes = kRows * 128 * DCH, kKvBytes = BN * 128 * DCH;
   static_assert(kRows * DCH * 64 * 4 <= 2 * kKvStages * kKvBytes, "the partial output takes the ring's place");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -97,6 +99,18 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
     ctl->abort_flag = 1;
     atomicOr(a.err, kErrTimeout);
   };
+  long long klast = a.Tk;                           // keys that some row of this CTA may see
+  if (a.causal) klast = max(0ll, min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift));
+  const int all = static_cast<int>((klast + BN - 1) / BN);
+  const int lo = static_cast<int>(static_cast<long long>(all) * rank / S);       // this CTA's tiles of keys
+  const int hi = static_cast<int>(static_cast<long long>(all) * (rank + 1) / S);
+  // without a mask every tile is taken, and what there is to know of it follows from its number
+  const int tail = static_cast<int>(klast - static_cast<long long>(all - 1) * BN);   // keys of the last tile of all
+  auto words_of = [&](int t) { return t < all - 1 ? W : (tail + 31) / 32; };
+  // tiles below this one hold keys that every row of the CTA sees (but for the mask)
+  long long full = a.Tk;
+  if (a.causal) full = max(0ll, min(full, r0 + shift + 1));
+  const int seen = static_cast<int>(full / BN);
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->qfull, 1);
@@ -108,18 +122,20 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
     }
     for (int s = 0; s < kInfo; ++s) {
       mbar_init(&ctl->ifull[s], 1);
-      mbar_init(&ctl->iempty[s], 5);                // four softmax warps and the MMA thread
+      mbar_init(&ctl->iempty[s], kSoftWarps + 1);   // and the one that issues the products
     }
-    mbar_init(&ctl->sfull, 1);
-    mbar_init(&ctl->sread, 4);
-    mbar_init(&ctl->pready, 4);
+    for (int s = 0; s < kBufs; ++s) {
+      mbar_init(&ctl->sfull[s], 1);
+      mbar_init(&ctl->pready[s], kSoftWarps);       // one per buffer: a warp may be a tile ahead of another
+    }
     mbar_init(&ctl->pvdone, 1);
+    mbar_init(&ctl->odone, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, 256);
+    tmem_alloc(&ctl->tmem_base, kCols);
     tmem_relinquish();
   }
   __syncthreads();
@@ -128,12 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
 
   if (warp == 0) {
     // ---------------------------------------------------------------- tiles, key bits, TMA
-    long long klast = a.Tk;                         // keys that some row of this CTA may see
-    if (a.causal) klast = max(0ll, min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift));
-    const int all = static_cast<int>((klast + BN - 1) / BN);
-    const int lo = static_cast<int>(static_cast<long long>(all) * rank / S);
-    const int hi = static_cast<int>(static_cast<long long>(all) * (rank + 1) / S);
-    const uint8_t* mask = a.mask ? a.mask + b * a.mask_bs : nullptr;
+    const uint8_t* mask = MASK ? a.mask + b * a.mask_bs : nullptr;
     const int bq = a.kb_shared & 1 ? 0 : b, bk = a.kb_shared & 2 ? 0 : b, bv = a.kb_shared & 4 ? 0 : b;
     uint32_t n = 0;                                 // tiles handed on
     bool ok = true;
@@ -142,45 +153,46 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const long long key = static_cast<long long>(t) * BN + 32 * w + lane;
-        next[w] = t < hi && key < a.Tk && mask ? mask[key] : 0;
+        next[w] = t < hi && key < a.Tk ? mask[key] : 0;
       }
     };
-    if (mask) fetch(lo);
+    if (MASK) fetch(lo);
     for (int t = lo; t <= hi && ok; ++t) {
       const bool end = t == hi;
       const int k0 = t * BN;
-      uint32_t bits[W], any = 0, every = 0xffffffffu;
-      if (!end) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const bool live = k0 + 32 * w + lane < a.Tk && (!mask || next[w] != 0);
-          bits[w] = __ballot_sync(0xffffffffu, live);
-          any |= bits[w];
-          every &= bits[w];
-        }
-        if (mask) fetch(t + 1);
-        if (!any) continue;
-      }
-      const uint32_t is = n % kInfo;
-      if (n >= kInfo) {
-        const bool okw = mbar_wait_bounded(&ctl->iempty[is], ((n / kInfo) & 1) ^ 1, lim, abortp);
-        if (!__all_sync(0xffffffffu, okw)) ok = false;
-      }
-      if (ok && lane == 0) {
-        Info& f = ctl->info[is];
-        f.k0 = end ? -1 : k0;
+      if (MASK) {
+        uint32_t bits[W], any = 0, every = 0xffffffffu;
         if (!end) {
-          f.plain = every == 0xffffffffu && (!a.causal || k0 + BN - 1 <= r0 + shift);
-          f.words = 1;
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            f.bits[w] = bits[w];
-            if (bits[w]) f.words = w + 1;
+            bits[w] = __ballot_sync(0xffffffffu, next[w] != 0);
+            any |= bits[w];
+            every &= bits[w];
           }
+          fetch(t + 1);
+          if (!any) continue;
         }
-        mbar_arrive(&ctl->ifull[is]);
+        const uint32_t is = n % kInfo;
+        if (n >= kInfo) {
+          const bool okw = mbar_wait_bounded(&ctl->iempty[is], ((n / kInfo) & 1) ^ 1, lim, abortp);
+          if (!__all_sync(0xffffffffu, okw)) ok = false;
+        }
+        if (ok && lane == 0) {
+          Info& f = ctl->info[is];
+          f.k0 = end ? -1 : k0;
+          if (!end) {
+            f.plain = every == 0xffffffffu && t < seen;
+            f.words = 1;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              f.bits[w] = bits[w];
+              if (bits[w]) f.words = w + 1;
+            }
+          }
+          mbar_arrive(&ctl->ifull[is]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       if (end || !ok) break;
       if (lane == 0) {
         if (n == 0) {
@@ -219,183 +231,193 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- products (one thread)
-    if (lane == 0) {
-      const int dk = (a.D + 15) / 16;                                // K = 16 steps of the first product
-      const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);      // and N = the keys taken
-      const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
-      const uint64_t qd = umma_desc_sw128(smem_u32(smem)), kd = umma_desc_sw128(smem_u32(ks));
-      const uint64_t vd = desc_mn_sw128(smem_u32(vs), BN * 128);
-      bool ok = true, issued = false;
-      auto more = [&](uint32_t j) {                                  // words of tile j, 0: no more (its info slot is then done with)
-        const uint32_t is = j % kInfo;
-        if (!mbar_wait_bounded(&ctl->ifull[is], (j / kInfo) & 1, lim, abortp)) {
-          ok = false;
-          return 0;
-        }
-        const int words = ctl->info[is].k0 >= 0 ? ctl->info[is].words : 0;
-        mbar_arrive(&ctl->iempty[is]);
-        return words;
-      };
-      auto scores = [&](uint32_t j, int words) {
-        const uint32_t s = j % kKvStages;
-        if ((j == 0 && !mbar_wait_bounded(&ctl->qfull, 0, lim, abortp)) ||
-            !mbar_wait_bounded(&ctl->kfull[s], (j / kKvStages) & 1, lim, abortp)) {
-          ok = false;
-          return;
-        }
-        tc_fence_after();
-        for (int kk = 0; kk < dk; ++kk) {                            // four 32-byte steps per 64-column chunk
-          const uint32_t c = kk >> 2, o = (kk & 3) * 32;
-          umma_ss_f16(tmem, qd + ((c * kRows * 128 + o) >> 4), kd + ((s * kKvBytes + c * BN * 128 + o) >> 4),
-                      idesc_s | (static_cast<uint32_t>(words * 4) << 17), kk > 0 ? 1u : 0u);
-        }
-        issued = true;
-        umma_commit(&ctl->kempty[s]);
-        umma_commit(&ctl->sfull);
-      };
-      int words = more(0);
-      if (words) scores(0, words);
-      for (uint32_t j = 0; words && ok; ++j) {
-        const uint32_t s = j % kKvStages;
-        const int ahead = more(j + 1);
-        if (ahead) {                                                 // once tile j's scores are in registers
-          if (!mbar_wait_bounded(&ctl->sread, j & 1, lim, abortp)) ok = false;
-          if (ok) scores(j + 1, ahead);
-        }
-        if (!ok || !mbar_wait_bounded(&ctl->pready, j & 1, lim, abortp) ||
-            !mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int kk = 0; kk < 2 * words; ++kk)
-          umma_ts_f16(tmem + kColO, tmem + kColP + 8 * kk, vd + ((s * kKvBytes + kk * 2048) >> 4), idesc_o,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&ctl->vempty[s]);
-        umma_commit(&ctl->pvdone);
-        words = ahead;
-      }
-      if (!ok) give_up();
-      if (issued) {
-        umma_commit(&ctl->drain);
-        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
-      }
+    // ---------------------------------------------------------------- products
+    // The warp stays converged and one elected lane issues: descriptors then live in
+    // uniform registers (a lone thread needed 900 clocks to issue four products).
+    const int dk = (a.D + 15) / 16;
+    const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);        // and N = the keys taken
+    const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
+    const uint64_t qd = umma_desc_sw128(smem_u32(smem)), kd = umma_desc_sw128(smem_u32(ks));
+    const uint64_t vd = desc_mn_sw128(smem_u32(vs), BN * 128);
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw) && ok;
+      return ok;
+    };
+    auto more = [&](uint32_t j) {                                    // words of tile j, 0: no more (its info slot is then done with)
+      if (!MASK) return lo + static_cast<int>(j) < hi ? words_of(lo + static_cast<int>(j)) : 0;
+      const uint32_t is = j % kInfo;
+      if (!wait(&ctl->ifull[is], (j / kInfo) & 1)) return 0;
+      const int words = ctl->info[is].k0 >= 0 ? ctl->info[is].words : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->iempty[is]);
+      return words;
+    };
+    // Scores of tile j, in order behind the output product that last read their buffer.
+    auto scores = [&](uint32_t j, int words) {
+      const uint32_t s = j % kKvStages;
+      // columns past D are zeros in both operands, so whole 64-column chunks are multiplied
+#pragma unroll
+      for (int c = 0; c < DCH; ++c)
+        umma_ss_f16_x4_elect(tmem + 64 * (j % kBufs), qd + ((c * kRows * 128) >> 4), kd + ((s * kKvBytes + c * BN * 128) >> 4),
+                             idesc_s | (static_cast<uint32_t>(words * 4) << 17), c > 0 ? 1u : 0u);
+      issued = true;
+      umma_commit_elect(&ctl->sfull[j % kBufs]);
+      umma_commit_elect(&ctl->kempty[s]);
+    };
+    int words = more(0);
+    if (words && wait(&ctl->qfull, 0) && wait(&ctl->kfull[0], 0)) scores(0, words);
+    for (uint32_t j = 0; words && ok; ++j) {
+      const uint32_t s = j % kKvStages, ph = (j / kKvStages) & 1, sn = (j + 1) % kKvStages, phn = ((j + 1) / kKvStages) & 1;
+      const int ahead = more(j + 1);
+      if (!ok || (ahead && !wait(&ctl->kfull[sn], phn))) break;
+      if (kBufs == 2 && ahead) scores(j + 1, ahead);
+      if (!wait(&ctl->vfull[s], ph) || !wait(&ctl->pready[j % kBufs], (j / kBufs) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (w < words)
+          umma_ts_f16_x2_elect(tmem + kColO, tmem + 64 * (j % kBufs) + 16 * w, vd + ((s * kKvBytes + w * 4096) >> 4),
+                               2048 >> 4, idesc_o, (j > 0 || w > 0) ? 1u : 0u);
+      if (!ahead) umma_commit_elect(&ctl->odone);
+      if (kBufs == 2) umma_commit_elect(&ctl->pvdone);               // else the next tile's scores say it
+      if (kBufs == 1 && ahead) scores(j + 1, ahead);
+      umma_commit_elect(&ctl->vempty[s]);
+      words = ahead;
+    }
+    if (!ok && lane == 0) give_up();
+    if (issued) {                                                    // what was issued ends before the CTA does
+      umma_commit_elect(&ctl->drain);
+      if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax: one row per thread
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int ochunks = (a.D + 15) / 16;
     float m = -INFINITY, l = 0.f;                   // the maximum that the weights are taken against, their sum
     uint32_t j = 0;
     bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw) && ok;
+      return ok;
+    };
     for (;; ++j) {
-      const uint32_t is = j % kInfo;
-      bool okw = mbar_wait_bounded(&ctl->ifull[is], (j / kInfo) & 1, lim, abortp);
-      if (!__all_sync(0xffffffffu, okw)) {
-        ok = false;
-        break;
-      }
-      const int k0 = ctl->info[is].k0;
-      const bool plain = ctl->info[is].plain != 0;
-      const int words = ctl->info[is].words;
+      bool plain;
+      int words, k0;
       uint32_t bits[W], hidden = 0;
-      if (k0 >= 0 && !plain) {
+      if (MASK) {
+        const uint32_t is = j % kInfo;
+        if (!wait(&ctl->ifull[is], (j / kInfo) & 1)) break;
+        const Info& f = ctl->info[is];
+        k0 = f.k0;
+        plain = f.plain != 0;
+        words = f.words;
+        if (k0 >= 0 && !plain) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) bits[w] = ctl->info[is].bits[w];
-        // the key of this thread when it zeroes a row of V
-        hidden = r < BN ? !((ctl->info[is].bits[r >> 5 & (W - 1)] >> lane) & 1u) : 0u;
-        if (a.causal) {
-          const long long vis = r0 + r + shift - k0 + 1;             // keys of the tile up to the diagonal
-          const int v = static_cast<int>(max(0ll, min(vis, static_cast<long long>(BN))));
+          for (int w = 0; w < W; ++w) bits[w] = f.bits[w];
+          hidden = r < BN ? !((f.bits[r >> 5 & (W - 1)] >> lane) & 1u) : 0u;   // this thread's row of V goes
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->iempty[is]);
+        if (k0 < 0) break;
+      } else {
+        const int t = lo + static_cast<int>(j);
+        if (t >= hi) break;
+        k0 = t * BN;
+        words = words_of(t);
+        plain = t < seen;
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const int c = min(max(v - 32 * w, 0), 32);
-            bits[w] &= c == 32 ? 0xffffffffu : (1u << c) - 1u;
-          }
+        for (int w = 0; w < W; ++w) bits[w] = 0xffffffffu;
+      }
+      if (!plain) {                                 // keys of the tile up to the last one, and up to the diagonal
+        long long vis = static_cast<long long>(a.Tk) - k0;
+        if (a.causal) vis = min(vis, r0 + r + shift - k0 + 1);
+        const int v = static_cast<int>(max(0ll, min(vis, static_cast<long long>(BN))));
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int c = min(max(v - 32 * w, 0), 32);
+          bits[w] &= c == 32 ? 0xffffffffu : (1u << c) - 1u;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->iempty[is]);
-      if (k0 < 0) break;
-      okw = mbar_wait_bounded(&ctl->sfull, j & 1, lim, abortp);
-      if (!__all_sync(0xffffffffu, okw)) {
-        ok = false;
-        break;
-      }
+      if (!wait(&ctl->sfull[j % kBufs], (j / kBufs) & 1)) break;
       tc_fence_after();
-      // the tile's scores, into registers: the next tile's may then take their place
-      float x[BN];
+      const uint32_t scores = lane_base + 64 * (j % kBufs);
+      // Groups of 16 scores, each on its way while the one before is worked on; first for the maximum.
+      uint32_t v[2][16];
+      auto hide = [&](uint32_t(&x)[16], int g) {
+        const uint32_t b16 = bits[g >> 1] >> (16 * (g & 1));
 #pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (w < words) tmem_ld_32x32b_x32(lane_base + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]));
-#pragma unroll
-      for (int w = 0; w < W; ++w) tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]));
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->sread);
-      if (!plain) {
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[32 * w + e] = (bits[w] >> e) & 1u ? x[32 * w + e] : -INFINITY;
-      }
+        for (int e = 0; e < 16; ++e)
+          if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;   // -inf
+      };
       float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_ld_32x32b_x16(scores, v[0]);
 #pragma unroll
-      for (int e = 0; e < BN; ++e) t4[e & 3] = fmaxf(t4[e & 3], x[e]);
-      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      // P and O are free once the last tile's second product is done
-      if (j > 0) {
-        okw = mbar_wait_bounded(&ctl->pvdone, (j - 1) & 1, lim, abortp);
-        if (!__all_sync(0xffffffffu, okw)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      for (int g = 0; g < 2 * W; ++g) {
+        if (g >= 2 * words) continue;
+        uint32_t(&x)[16] = v[g & 1];
+        tmem_wait_ld_regs(x);
+        if (g + 1 < 2 * W && g + 1 < 2 * words) tmem_ld_32x32b_x16(scores + 16 * (g + 1), v[(g + 1) & 1]);
+        if (!plain) hide(x, g);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
       }
-      const bool grow = top > m && !((top - m) * a.scale_log2 <= kGrow);
+      const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);   // NaN if any score is
+      const bool grow = !((top - m) * a.scale_log2 <= kGrow);   // also for NaN, and where there was no key before
       if (__any_sync(0xffffffffu, grow)) {
-        const float mn = fmaxf(m, top);
+        float mn = max3_nan(m, top, top);
+        if (mn == INFINITY) mn = NAN;               // infinity against infinity: the row is NaN
         const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
         m = mn;
         l *= f;
         if (j > 0) {
-          for (int c = 0; c < (a.D + 15) / 16; ++c) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
-            tmem_wait_ld_regs(v);
+          // O is at rest: the product before the last ended before these scores were
+          // formed, and with one buffer the last one did too
+          if (kBufs == 2 && !wait(&ctl->pvdone, (j - 1) & 1)) break;
+          tc_fence_after();
+          for (int c = 0; c < ochunks; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
+            tmem_wait_ld_regs(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st_32x32b_x16(lane_base + kColO + 16 * c, v);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x16(lane_base + kColO + 16 * c, o);
           }
         }
       }
       const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
-      // the weights
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), base2 = make_float2(-base, -base);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      tmem_ld_32x32b_x16(scores, v[0]);             // and again for the weights
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w >= words) continue;
-        uint32_t p[16];
+      for (int g = 0; g < 2 * W; ++g) {
+        if (g >= 2 * words) continue;
+        uint32_t(&x)[16] = v[g & 1];
+        tmem_wait_ld_regs(x);
+        if (g + 1 < 2 * W && g + 1 < 2 * words) tmem_ld_32x32b_x16(scores + 16 * (g + 1), v[(g + 1) & 1]);
+        if (!plain) hide(x, g);
+        uint32_t p[8];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          x[32 * w + e] = ex2_approx(fmaf(x[32 * w + e], a.scale_log2, -base));
-          sum[e & 3] += x[32 * w + e];
+        for (int e = 0; e < 8; ++e) {
+          float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, base2);
+          y.x = ex2_approx(y.x);
+          y.y = ex2_approx(y.y);
+          sum[e & 1] = add2(sum[e & 1], y);
+          p[e] = pack_bf16x2(y.x, y.y);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(x[32 * w + 2 * e], x[32 * w + 2 * e + 1]);
-        tmem_st_32x32b_x16(lane_base + kColP + 16 * w, p);
+        tmem_st_32x32b_x8(scores + 8 * g, p);       // over scores that are done with: 8 g + 8 <= 16 g + 16
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
       tmem_wait_st();
-      if (!plain) {                                 // rows of V that no row may see
+      if (MASK && !plain) {                         // rows of V that no row may see
         const uint32_t s = j % kKvStages;
-        okw = mbar_wait_bounded(&ctl->vfull[s], (j / kKvStages) & 1, lim, abortp);
-        if (!__all_sync(0xffffffffu, okw)) {
-          ok = false;
-          break;
-        }
+        if (!wait(&ctl->vfull[s], (j / kKvStages) & 1)) break;
         if (hidden) {
           for (int c = 0; c < DCH; ++c)
 #pragma unroll
@@ -406,26 +428,29 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->pready);
+      if (lane == 0) mbar_arrive(&ctl->pready[j % kBufs]);
     }
     if (ok && j > 0) {
-      const bool okw = mbar_wait_bounded(&ctl->pvdone, (j - 1) & 1, lim, abortp);
-      ok = __all_sync(0xffffffffu, okw);
+      wait(&ctl->odone, 0);
       tc_fence_after();
     }
     if (!ok && lane == 0) give_up();
     const bool mine = ok && r0 + r < a.Tq;
-    if (S == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs;
-      for (int c = 0; c < (a.D + 15) / 16; ++c) {
-        uint32_t v[16];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs;
+    if (S > 1) {
+      ctl->m[r] = m;
+      ctl->l[r] = l;
+    }
+    for (int c = 0; c < ochunks; ++c) {
+      uint32_t v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0u;
-        if (ok && j > 0) {
-          tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
-          tmem_wait_ld_regs(v);
-        }
+      for (int e = 0; e < 16; ++e) v[e] = 0u;
+      if (ok && j > 0) {
+        tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
+        tmem_wait_ld_regs(v);
+      }
+      if (S == 1) {
         if (!mine) continue;
 #pragma unroll
         for (int e = 0; e < 16; e += 8) {
@@ -436,20 +461,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
             w[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv, __uint_as_float(v[e + 2 * i + 1]) * inv);
           *reinterpret_cast<uint4*>(o + 16 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
-    } else {
-      // this CTA's share, over the K and V ring (its last reader, the last product, is done):
-      // row r's 16-byte pieces c at c ^ (r & 15), so that the 32 rows of a store spread over the banks
-      ctl->m[r] = m;
-      ctl->l[r] = l;
-      for (int c = 0; c < (a.D + 15) / 16; ++c) {
-        uint32_t v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0u;
-        if (ok && j > 0) {
-          tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, v);
-          tmem_wait_ld_regs(v);
-        }
+      } else {
+        // this CTA's share, over the K and V ring (its last reader, the last product, is done):
+        // row r's 16-byte pieces c at c ^ (r & 15), so that the 32 rows of a store spread over the banks
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<uint4*>(ks + r * (256 * DCH) + (((4 * c + e) ^ (r & 15)) << 4)) =
@@ -462,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const __grid_con
   // tensor memory is given back before any wait for another CTA
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, kCols);
   }
   if (S > 1) {
     cluster_sync();
@@ -516,11 +530,11 @@ bool encode(CUtensorMap* m, const HeadsView& t, int B, int rows, int D, int box_
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DCH>
+template <int DCH, bool MASK>
 cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
-  constexpr size_t bytes = 1024 + kRows * 128 * DCH + 2 * kKvStages * kKvBytes + sizeof(Ctl);
-  static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DCH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  constexpr size_t bytes = 1024 + kRows * 128 * DCH + 2 * kKvStages * BN * 128 * DCH + sizeof(Ctl);
+  static_assert((DCH == 1 ? 4 : 2) * (bytes + 1024) <= 228 * 1024, "CTAs per SM");
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DCH, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -534,7 +548,7 @@ cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel<DCH>, a, S);
+  return cudaLaunchKernelEx(&cfg, attention_kernel<DCH, MASK>, a, S);
 }
 
 }  // namespace atc
@@ -549,9 +563,8 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_
     return cudaGetLastError();
   }
   Args p{};
-  const int bn = a.D <= 64 ? 128 : 64;
-  if (!encode(&p.q, a.q, a.B, a.Tq, a.D, kRows) || !encode(&p.k, a.k, a.B, a.Tk, a.D, bn) ||
-      !encode(&p.v, a.v, a.B, a.Tk, a.D, bn)) {
+  if (!encode(&p.q, a.q, a.B, a.Tq, a.D, kRows) || !encode(&p.k, a.k, a.B, a.Tk, a.D, BN) ||
+      !encode(&p.v, a.v, a.B, a.Tk, a.D, BN)) {
     *why = "tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -573,10 +586,12 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
   const long long work = static_cast<long long>(p.ntiles) * a.q.heads * a.B;
-  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + bn - 1) / bn);
+  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + BN - 1) / BN);
   int S = 1;
   while (S < 8 && work * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
-  return a.D <= 64 ? go<1>(p, S, static_cast<unsigned>(work), stream) : go<2>(p, S, static_cast<unsigned>(work), stream);
+  const unsigned w = static_cast<unsigned>(work);
+  if (a.mask) return a.D <= 64 ? go<1, true>(p, S, w, stream) : go<2, true>(p, S, w, stream);
+  return a.D <= 64 ? go<1, false>(p, S, w, stream) : go<2, false>(p, S, w, stream);
 }
 
 }  // namespace gkd
