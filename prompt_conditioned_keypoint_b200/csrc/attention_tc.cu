@@ -78,6 +78,7 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t l
 template <int DCH, bool MASK>
 __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(const __grid_constant__ Args a, int S) {
   constexpr int kBufs = DCH;                                         // buffers of scores
+  constexpr bool kHold = DCH == 2;                                   // 128 registers and more a thread
   constexpr uint32_t kCols = 128 * DCH, kColO = 64 * kBufs;          // scores at 0 (and 64)
   constexpr int kQBytes = kRows * 128 * DCH, kKvBytes = BN * 128 * DCH;
   static_assert(kRows * DCH * 64 * 4 <= 2 * kKvStages * kKvBytes, "the partial output takes the ring's place");
@@ -346,8 +347,10 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       if (!wait(&ctl->sfull[j % kBufs], (j / kBufs) & 1)) break;
       tc_fence_after();
       const uint32_t scores = lane_base + 64 * (j % kBufs);
-      // Groups of 16 scores, each on its way while the one before is worked on; first for the maximum.
-      uint32_t v[2][16];
+      // Groups of 16 scores. With two CTAs per SM a tile's scores stay in registers; with
+      // four they are read twice, for the maximum and for the weights, and a group is on
+      // its way while the one before is worked on.
+      uint32_t v[kHold ? 2 * W : 2][16];
       auto hide = [&](uint32_t(&x)[16], int g) {
         const uint32_t b16 = bits[g >> 1] >> (16 * (g & 1));
 #pragma unroll
@@ -355,13 +358,19 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
           if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;   // -inf
       };
       float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      tmem_ld_32x32b_x16(scores, v[0]);
+      auto load = [&](int g) { tmem_ld_32x32b_x16(scores + 16 * g, v[kHold ? g : g & 1]); };
+      load(0);
+      if (kHold) {
+#pragma unroll
+        for (int g = 1; g < 2 * W; ++g)
+          if (g < 2 * words) load(g);
+      }
 #pragma unroll
       for (int g = 0; g < 2 * W; ++g) {
         if (g >= 2 * words) continue;
-        uint32_t(&x)[16] = v[g & 1];
+        uint32_t(&x)[16] = v[kHold ? g : g & 1];
         tmem_wait_ld_regs(x);
-        if (g + 1 < 2 * W && g + 1 < 2 * words) tmem_ld_32x32b_x16(scores + 16 * (g + 1), v[(g + 1) & 1]);
+        if (!kHold && g + 1 < 2 * W && g + 1 < 2 * words) load(g + 1);
         if (!plain) hide(x, g);
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
@@ -393,14 +402,16 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
       const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), base2 = make_float2(-base, -base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      tmem_ld_32x32b_x16(scores, v[0]);             // and again for the weights
+      if (!kHold) load(0);
 #pragma unroll
       for (int g = 0; g < 2 * W; ++g) {
         if (g >= 2 * words) continue;
-        uint32_t(&x)[16] = v[g & 1];
-        tmem_wait_ld_regs(x);
-        if (g + 1 < 2 * W && g + 1 < 2 * words) tmem_ld_32x32b_x16(scores + 16 * (g + 1), v[(g + 1) & 1]);
-        if (!plain) hide(x, g);
+        uint32_t(&x)[16] = v[kHold ? g : g & 1];
+        if (!kHold) {
+          tmem_wait_ld_regs(x);
+          if (g + 1 < 2 * W && g + 1 < 2 * words) load(g + 1);
+          if (!plain) hide(x, g);
+        }
         uint32_t p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
