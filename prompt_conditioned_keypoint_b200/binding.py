@@ -105,6 +105,22 @@ def _stream(s, ref=None) -> int | None:
     return s.cuda_stream
 
 
+_raw_stream = None
+
+
+def _stream_fast(s, ref=None) -> int | None:
+    """_stream for calls of a few microseconds: torch's raw query of its current
+    stream, where it has one, builds no Stream object (0.3 instead of 2.6 us)."""
+    global _raw_stream
+    dev = getattr(ref, "device", None)
+    if s is not None or dev is None or dev.type != "cuda" or dev.index is None:
+        return _stream(s, ref)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+    return _raw_stream(dev.index) if _raw_stream is not _stream else _stream(s, ref)
+
+
 def _check(fn: str, status: int):
     if status != GKD_OK:
         raise GkdError(status, fn, gkd_last_error())
@@ -205,7 +221,7 @@ def gkd_linear(x, dt, T, Cin, x_stride, weight, Cout, bias, act, scale, residual
                out_stride, stream=None):
     _check("gkd_linear", lib.gkd_linear(
         _ptr(x), dt, T, Cin, x_stride, _ptr(weight), Cout, _ptr(bias), act, _ptr(scale), _ptr(residual),
-        residual_stride, _ptr(out), out_dt, out_stride, _stream(stream, x)))
+        residual_stride, _ptr(out), out_dt, out_stride, _stream_fast(stream, x)))
 
 
 def gkd_qk_norm_rope(q, k, dt, B, T, D, q_weight, k_weight, eps, pos, pos_batch_stride, axes, pair_axis, pair_freq,
@@ -214,11 +230,11 @@ def gkd_qk_norm_rope(q, k, dt, B, T, D, q_weight, k_weight, eps, pos, pos_batch_
     _check("gkd_qk_norm_rope", lib.gkd_qk_norm_rope(
         gkd_heads(q), gkd_heads(k), dt, B, T, D, _ptr(q_weight), _ptr(k_weight), eps, _ptr(pos), pos_batch_stride,
         axes, _ptr(pair_axis), _ptr(pair_freq), pairs, interleaved, gkd_heads(q_out), gkd_heads(k_out),
-        _stream(stream, q)))
+        _stream_fast(stream, q)))
 
 
 def gkd_attention(q, k, v, dt, B, Tq, Tk, D, scale, causal, key_mask, key_mask_batch_stride, out, stream=None):
     """q, k, v and out: tensors [B][rows][heads][D], or GkdHeads views."""
     _check("gkd_attention", lib.gkd_attention(
         gkd_heads(q), gkd_heads(k), gkd_heads(v), dt, B, Tq, Tk, D, scale, causal, _ptr(key_mask),
-        key_mask_batch_stride, gkd_heads(out), _stream(stream, q)))
+        key_mask_batch_stride, gkd_heads(out), _stream_fast(stream, q)))

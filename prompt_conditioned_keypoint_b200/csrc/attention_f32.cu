@@ -161,8 +161,7 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
 template <int DC>
 cudaError_t go(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
   constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * 68);
-  cudaError_t e = cudaFuncSetAttribute(attention_f32_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bytes));
+  cudaError_t e = allow_smem<attention_f32_kernel<DC>>(bytes);
   if (e != cudaSuccess) return e;
   attention_f32_kernel<DC><<<grid, kThreads, bytes, stream>>>(a);
   return cudaGetLastError();

@@ -545,8 +545,7 @@ template <int DCH, bool MASK>
 cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
   constexpr size_t bytes = 1024 + kRows * 128 * DCH + 2 * kKvStages * BN * 128 * DCH + sizeof(Ctl);
   static_assert((DCH == 1 ? 4 : 2) * (bytes + 1024) <= 228 * 1024, "CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<DCH, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bytes));
+  cudaError_t e = allow_smem<attention_kernel<DCH, MASK>>(bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(work * S);

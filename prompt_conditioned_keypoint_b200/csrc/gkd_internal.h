@@ -2,6 +2,7 @@
 // Every launcher assumes its arguments were validated by the caller and only
 // enqueues work on `stream`; it returns the CUDA launch status.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -108,6 +109,20 @@ cudaError_t launch_pool_tc(const float* support, int B, int h, int w, int C, con
 // ---------------------------------------------------------------------------
 // Operators of the transformer blocks (gkd_blocks.h)
 // ---------------------------------------------------------------------------
+// Allows a kernel its dynamic shared memory, once per kernel and device.
+template <auto* Kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};    // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 struct LinearArgs {
   const void* x;
   const void* weight;        // [Cout][Cin]
@@ -139,7 +154,9 @@ struct RopeArgs {
   long long pos_bs;
   const uint8_t* pair_axis;
   const float* pair_freq;
-  int tok, log_lanes;        // set by the launcher: rows per CTA, log2 of the lanes per head
+  int tok, fold;             // set by the launcher: rows per CTA, first step of the sum over a head's lanes
+  unsigned heads_magic;      // to divide by the heads of a row
+  float inv_d;
 };
 cudaError_t launch_qk_norm_rope(RopeArgs& g, bool bf16, int num_sms, cudaStream_t stream);
 

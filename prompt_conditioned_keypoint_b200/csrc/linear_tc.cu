@@ -517,8 +517,7 @@ bool encode(CUtensorMap* m, bool bf16, const void* base, long long cols, long lo
 
 template <bool F32OUT, bool RES>
 cudaError_t go_rows(const RowsArgs& r, unsigned grid, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<F32OUT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(Ring<RES>::kSmem));
+  cudaError_t e = allow_smem<rows_kernel<F32OUT, RES>>(Ring<RES>::kSmem);
   if (e != cudaSuccess) return e;
   rows_kernel<F32OUT, RES><<<grid, kThreads, Ring<RES>::kSmem, stream>>>(r);
   return cudaGetLastError();
@@ -551,8 +550,7 @@ cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, c
 template <int N, typename TO>
 cudaError_t go_split(const SplitArgs& p, int S, unsigned ctiles, unsigned rtiles, cudaStream_t stream) {
   constexpr size_t bytes = split_smem<N>();
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<N, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bytes));
+  cudaError_t e = allow_smem<split_kernel<N, TO>>(bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctiles * S, rtiles);

@@ -138,3 +138,14 @@ def test_binding_raises_with_the_librarys_message():
         gk.gkd_linear(x, F32, 4, 60, 60, x, 32, None, gk.GKD_ACT_NONE, None, None, 0, x, F32, 32, stream=0)
     assert e.value.status == SHAPE and "Cin=60" in str(e.value)
     assert ctypes.sizeof(gk.GkdHeads) == 40
+
+
+def test_block_calls_follow_the_first_tensors_device(monkeypatch):
+    class OnDevice:
+        device = torch.device("cuda", 3)
+
+    monkeypatch.setattr(gk, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(gk, "_stream", lambda s, ref=None: -1 if s is None else s)
+    assert gk._stream_fast(None, OnDevice()) == 1003
+    assert gk._stream_fast(77, OnDevice()) == 77
+    assert gk._stream_fast(None, torch.zeros(4)) == -1 and gk._stream_fast(None, 12345) == -1 and gk._stream_fast(None) == -1
