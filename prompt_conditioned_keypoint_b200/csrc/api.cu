@@ -612,12 +612,13 @@ gkd_status gkd_linear(const void* x, gkd_dtype dt, int T, int Cin, long long x_s
   a.Cin = Cin;
   a.Cout = Cout;
   a.act = act;
-  a.in_bf16 = dt == GKD_BF16;
   a.out_bf16 = out_dt == GKD_BF16;
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
   const char* why = "";
-  cudaError_t e = gkd::launch_linear(a, ds->num_sms, static_cast<cudaStream_t>(stream), &why);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dt == GKD_BF16 ? gkd::launch_linear_tc(a, ds->num_sms, st, &why)
+                                       : gkd::launch_linear_f32(a, ds->num_sms, st, &why);
   if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "linear: %s", why);
   return launched(e, "linear");
 }

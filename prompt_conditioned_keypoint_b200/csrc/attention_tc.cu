@@ -547,18 +547,7 @@ cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
   static_assert((DCH == 1 ? 4 : 2) * (bytes + 1024) <= 228 * 1024, "CTAs per SM");
   cudaError_t e = allow_smem<attention_kernel<DCH, MASK>>(bytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(work * S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel<DCH, MASK>, a, S);
+  return launch_cluster(attention_kernel<DCH, MASK>, dim3(work * S), kThreads, bytes, S, stream, a, S);
 }
 
 }  // namespace atc

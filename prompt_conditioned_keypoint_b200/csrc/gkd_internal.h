@@ -123,6 +123,28 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
+// Launches clusters of S CTAs along x.
+template <typename... Params, typename... Given>
+cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int S, cudaStream_t stream,
+                           const Given&... given) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
+}
+
+// Tensor map of a [rows][cols] tensor whose rows are `stride` elements apart; 128B-swizzled boxes.
+bool encode_rows(CUtensorMap* m, bool bf16, const void* base, long long cols, long long rows, long long stride,
+                 int box_cols, int box_rows);
+
 struct LinearArgs {
   const void* x;
   const void* weight;        // [Cout][Cin]
@@ -132,11 +154,11 @@ struct LinearArgs {
   void* out;
   long long x_stride, residual_stride, out_stride;   // elements between rows
   int T, Cin, Cout, act;
-  bool in_bf16, out_bf16;
+  bool out_bf16;
   unsigned* err;
   unsigned long long wait_limit_ns;
 };
-cudaError_t launch_linear(LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);
+cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16 operands
 
 struct RopeSide {            // q or k

@@ -1,73 +1,273 @@
-// gkd_linear on the fp32 units, fp32 operands: out = residual + scale * act(x weight^T + bias).
+// gkd_linear for fp32 operands: out = residual + scale * act(x weight^T + bias) on the
+// tensor cores, with fp32 accuracy from TF32 products.
+//
+// Every operand is taken as x = hi + lo: hi is x without its low 13 bits (which
+// kind::tf32 does not read, so hi needs no copy), lo = x - hi rounded to TF32. Then
+// x w = hi hi + hi lo + lo hi to within 2^-20 of |x w|, three products per term, where
+// the fp32 units have a sixth of one product's rate.
+// The tensor core truncates each step's sum, so a long sum drifts towards zero (at 1024
+// channels by 2.4e-6 of the result for plain TF32): the large products and the small
+// ones have accumulators of their own, and the epilogue warps add both up in fp32
+// after every 64 channels. Measured error at 1024 channels: 00 (fp32 fused
+// multiply-adds: 2.5e-7).
+//
+// A CTA has a 128 x 128 tile of the output, 18 warps:
+//   warp 0       TMA: stages of 32 channels of x and of weight (128B-swizzled);
+//   warp 1       products, 12 per stage, into two pairs of accumulators in turn;
+//   warps 2-9    lo tiles: 16 bytes in, 16 bytes out at the same place of the next tile,
+//                whatever the swizzle;
+//   warps 10-17  sums in registers (a thread: one row, 64 columns).
+// Few tiles: a cluster of S CTAs shares a tile's channels; the sums meet in shared
+// memory in rank order and every CTA finishes its share of the rows.
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
 namespace gkd {
-namespace lin {
+namespace lin32 {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kTile = 128, kChunk = 32, kStages = 3, kFlush = 2;   // stages per accumulator: 64 channels
+constexpr int kOpBytes = kTile * 128;                              // one operand's tile of a stage
+constexpr int kStageBytes = 4 * kOpBytes;                          // x, weight, and their lo parts
+constexpr int kConvWarps = 8, kSumWarps = 8, kThreads = 32 * (2 + kConvWarps + kSumWarps);
 
-// One 64 x 64 tile of the output per CTA, a 4 x 4 patch per thread; the channels
-// go through shared memory 16 at a time.
-__global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ LinearArgs a) {
-  __shared__ float xs[kStep][kTile + 4], ws[kStep][kTile + 4];
-  const int t0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
-  const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
-  const float* x = static_cast<const float*>(a.x);
-  const float* w = static_cast<const float*>(a.weight);
-  float acc[4][4] = {};
-  const int lr = tid >> 2, lc = (tid & 3) * 4;
-  for (int c0 = 0; c0 < a.Cin; c0 += kStep) {
-    float4 xv = make_float4(0.f, 0.f, 0.f, 0.f), wv = xv;
-    if (c0 + lc < a.Cin) {
-      if (t0 + lr < a.T) xv = load4(x + static_cast<long long>(t0 + lr) * a.x_stride + c0 + lc);
-      if (n0 + lr < a.Cout) wv = load4(w + static_cast<long long>(n0 + lr) * a.Cin + c0 + lc);
-    }
-    __syncthreads();
-    xs[lc][lr] = xv.x; xs[lc + 1][lr] = xv.y; xs[lc + 2][lr] = xv.z; xs[lc + 3][lr] = xv.w;
-    ws[lc][lr] = wv.x; ws[lc + 1][lr] = wv.y; ws[lc + 2][lr] = wv.z; ws[lc + 3][lr] = wv.w;
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kStep; ++c) {
-      const float4 p = *reinterpret_cast<const float4*>(&xs[c][tr * 4]);
-      const float4 q = *reinterpret_cast<const float4*>(&ws[c][tc * 4]);
-      const float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(pv[i], qv[j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + tr * 4 + i, n = n0 + tc * 4;
-    if (t >= a.T || n >= a.Cout) continue;                         // Cout is a multiple of 8
-    float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.residual)
-      res = load4(static_cast<const float*>(a.residual) + static_cast<long long>(t) * a.residual_stride + n);
-    const float rv[4] = {res.x, res.y, res.z, res.w};
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = acc[i][j] + (a.bias ? a.bias[n + j] : 0.f);
-    }
-    activate(y, a.act);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (a.scale) y[j] *= a.scale[n + j];
-      y[j] += rv[j];
-    }
-    store4(static_cast<float*>(a.out) + static_cast<long long>(t) * a.out_stride + n, make_float4(y[0], y[1], y[2], y[3]));
-  }
+struct Args {
+  CUtensorMap x, w;
+  const float* bias;
+  const float* scale;
+  const float* residual;
+  float* out;
+  long long residual_stride, out_stride;
+  int T, Cin, Cout, act;
+  unsigned* err;
+  unsigned long long wait_limit_ns;
+};
+
+struct Ctl {
+  uint64_t full[kStages], ready[kStages], empty[kStages], accfull[2], accempty[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + sizeof(Ctl);
+static_assert(kTile * kTile * 4 <= kStages * kStageBytes, "the sums take the ring's place");
+
+__device__ __forceinline__ float lo_part(float x) {
+  const float lo = x - __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(lo));
+  return __uint_as_float(r);
 }
 
-}  // namespace lin
+__global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_constant__ Args a, int S) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kStages * kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S;                                 // = the rank in the cluster
+  const int ncol = (a.Cout + kTile - 1) / kTile;
+  const int tile = blockIdx.x / S;
+  const int t0 = tile / ncol * kTile, n0 = tile % ncol * kTile;
+  const int nkall = (a.Cin + kChunk - 1) / kChunk;
+  const int kb = static_cast<int>(static_cast<long long>(nkall) * rank / S);
+  const int nk = static_cast<int>(static_cast<long long>(nkall) * (rank + 1) / S) - kb;   // may be 0
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abortp = &ctl->abort_flag;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+    ok = __all_sync(0xffffffffu, okw) && ok;
+    return ok;
+  };
+  auto give_up = [&] {
+    if (lane == 0) {
+      ctl->abort_flag = 1;
+      atomicOr(a.err, kErrTimeout);
+    }
+  };
 
-cudaError_t launch_linear(LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
-  if (a.in_bf16) return launch_linear_tc(a, num_sms, stream, why);
-  const dim3 grid((a.T + lin::kTile - 1) / lin::kTile, (a.Cout + lin::kTile - 1) / lin::kTile);
-  lin::linear_kernel<<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->ready[s], kConvWarps);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->accfull[s], 1);
+      mbar_init(&ctl->accempty[s], kSumWarps);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == 0) {
+    int it = 0;
+    for (; it < nk; ++it) {
+      const int s = it % kStages;
+      if (it >= kStages && !wait(&ctl->empty[s], ((it / kStages) & 1) ^ 1)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl->full[s], 2 * kOpBytes);
+        tma_load_2d(smem + s * kStageBytes, &a.x, &ctl->full[s], (kb + it) * kChunk, t0);
+        tma_load_2d(smem + s * kStageBytes + kOpBytes, &a.w, &ctl->full[s], (kb + it) * kChunk, n0);
+      }
+      __syncwarp();
+    }
+    if (!ok) give_up();
+    for (int k = 0; k < kStages && k < it; ++k) {
+      const int last = it - 1 - k;
+      if (!mbar_wait_drain(&ctl->full[last % kStages], (last / kStages) & 1, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // fp32 accumulator, tf32 x tf32, both K-major, M = N = 128
+    constexpr uint32_t idesc = (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
+    const uint64_t base = umma_desc_sw128(smem_u32(smem));
+    int it = 0, acc = 0;
+    for (; it < nk; ++it) {
+      const int s = it % kStages, buf = acc & 1;
+      const bool fresh = it % kFlush == 0;
+      if (fresh && acc >= 2 && !wait(&ctl->accempty[buf], ((acc >> 1) & 1) ^ 1)) break;
+      if (!wait(&ctl->ready[s], (it / kStages) & 1)) break;
+      tc_fence_after();
+      const uint64_t x = base + ((s * kStageBytes) >> 4), w = x + (kOpBytes >> 4), xl = w + (kOpBytes >> 4), wl = xl + (kOpBytes >> 4);
+      const uint32_t big = tmem + 256 * buf, small = big + 128;
+      umma_ss_tf32_x4_elect(small, x, wl, idesc, fresh ? 0u : 1u);
+      umma_ss_tf32_x4_elect(small, xl, w, idesc, 1u);
+      umma_ss_tf32_x4_elect(big, x, w, idesc, fresh ? 0u : 1u);
+      umma_commit_elect(&ctl->empty[s]);
+      if (it % kFlush == kFlush - 1 || it == nk - 1) {
+        umma_commit_elect(&ctl->accfull[buf]);
+        ++acc;
+      }
+    }
+    if (!ok) give_up();
+    if (it > 0) {                                                  // what was issued ends before the CTA does
+      umma_commit_elect(&ctl->drain);
+      if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else if (warp < 2 + kConvWarps) {
+    const int tid = threadIdx.x - 64;
+    for (int it = 0; it < nk; ++it) {
+      const int s = it % kStages;
+      if (!wait(&ctl->full[s], (it / kStages) & 1)) break;
+      uint8_t* p = smem + s * kStageBytes + tid * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * kOpBytes / (16 * 32 * kConvWarps); ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + i * (16 * 32 * kConvWarps));
+        *reinterpret_cast<float4*>(p + i * (16 * 32 * kConvWarps) + 2 * kOpBytes) =
+            make_float4(lo_part(v.x), lo_part(v.y), lo_part(v.z), lo_part(v.w));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ready[s]);
+    }
+    if (!ok) give_up();
+  } else {
+    const int q = warp & 3, half = (warp - 2 - kConvWarps) >> 2, r = 32 * q + lane;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + 64 * half;
+    float v[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) v[j] = 0.f;
+    for (int k0 = 0, acc = 0; k0 < nk; k0 += kFlush, ++acc) {
+      const int buf = acc & 1;
+      if (!wait(&ctl->accfull[buf], (acc >> 1) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        uint32_t big[8], small[8];
+        tmem_ld_32x32b_x8(src0 + 256 * buf + 8 * g, big);
+        tmem_ld_32x32b_x8(src0 + 256 * buf + 128 + 8 * g, small);
+        tmem_wait_ld_regs(big);
+        tmem_wait_ld_regs(small);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * g + j] += __uint_as_float(big[j]) + __uint_as_float(small[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->accempty[buf]);
+    }
+    if (!ok) {
+      give_up();
+    } else {
+      // over the ring, which the last product has left; row r's 16-byte pieces c at c ^ (r & 31)
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<float4*>(smem + r * 512 + (((16 * half + c) ^ (r & 31)) << 4)) =
+            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // tensor memory is given back before any wait for another CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (S > 1) cluster_sync();
+  const int c = n0 + 4 * lane;
+  if (c < a.Cout) {
+    const uint32_t base = smem_u32(smem);
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f), sc = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (a.bias) b = *reinterpret_cast<const float4*>(a.bias + c);
+    if (a.scale) sc = *reinterpret_cast<const float4*>(a.scale + c);
+    for (int r = rank * (kTile / S) + warp; r < (rank + 1) * (kTile / S) && t0 + r < a.T; r += kThreads / 32) {
+      const long long t = t0 + r;
+      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.residual) res = load4(a.residual + t * a.residual_stride + c);
+      const uint32_t at = r * 512 + ((lane ^ (r & 31)) << 4);
+      float z[4] = {b.x, b.y, b.z, b.w};
+      for (int s = 0; s < S; ++s) {
+        const float4 v = S > 1 ? cluster_load4(cluster_map(base + at, s)) : *reinterpret_cast<const float4*>(smem + at);
+        z[0] += v.x;
+        z[1] += v.y;
+        z[2] += v.z;
+        z[3] += v.w;
+      }
+      activate(z, a.act);
+      store4(a.out + t * a.out_stride + c, make_float4(fmaf(sc.x, z[0], res.x), fmaf(sc.y, z[1], res.y),
+                                                       fmaf(sc.z, z[2], res.z), fmaf(sc.w, z[3], res.w)));
+    }
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync();                                       // nobody leaves while its shared memory is read
+}
+
+}  // namespace lin32
+
+cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
+  using namespace lin32;
+  Args p{};
+  if (!encode_rows(&p.x, false, a.x, a.Cin, a.T, a.x_stride, kChunk, kTile) ||
+      !encode_rows(&p.w, false, a.weight, a.Cin, a.Cout, a.Cin, kChunk, kTile)) {
+    *why = "tensor map encoding failed";
+    return cudaErrorInvalidValue;
+  }
+  p.bias = a.bias;
+  p.scale = a.scale;
+  p.residual = static_cast<const float*>(a.residual);
+  p.out = static_cast<float*>(a.out);
+  p.residual_stride = a.residual_stride;
+  p.out_stride = a.out_stride;
+  p.T = a.T;
+  p.Cin = a.Cin;
+  p.Cout = a.Cout;
+  p.act = a.act;
+  p.err = a.err;
+  p.wait_limit_ns = a.wait_limit_ns;
+  const long long tiles = (static_cast<long long>(a.T) + kTile - 1) / kTile * ((a.Cout + kTile - 1) / kTile);
+  const int nk = (a.Cin + kChunk - 1) / kChunk;
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= num_sms && nk >= 4 * S) S *= 2;
+  cudaError_t e = allow_smem<linear_f32_kernel>(kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(linear_f32_kernel, dim3(static_cast<unsigned>(tiles * S)), kThreads, kSmem, S, stream, p, S);
 }
 
 }  // namespace gkd

@@ -503,18 +503,6 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-bool encode(CUtensorMap* m, bool bf16, const void* base, long long cols, long long rows, long long stride, int box_cols,
-            int box_rows) {
-  EncodeTiledFn enc = get_encode_tiled();
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (bf16 ? 2 : 4)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
-  return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                    const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool F32OUT, bool RES>
 cudaError_t go_rows(const RowsArgs& r, unsigned grid, cudaStream_t stream) {
   cudaError_t e = allow_smem<rows_kernel<F32OUT, RES>>(Ring<RES>::kSmem);
@@ -526,10 +514,10 @@ cudaError_t go_rows(const RowsArgs& r, unsigned grid, cudaStream_t stream) {
 cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
   RowsArgs r{};
   const int cols = a.out_bf16 ? 64 : 32;
-  if (!encode(&r.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, kM) ||
-      !encode(&r.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, kN) ||
-      !encode(&r.out, a.out_bf16, a.out, a.Cout, a.T, a.out_stride, cols, 32) ||
-      (a.residual && !encode(&r.res, a.out_bf16, a.residual, a.Cout, a.T, a.residual_stride, cols, 32))) {
+  if (!encode_rows(&r.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, kM) ||
+      !encode_rows(&r.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, kN) ||
+      !encode_rows(&r.out, a.out_bf16, a.out, a.Cout, a.T, a.out_stride, cols, 32) ||
+      (a.residual && !encode_rows(&r.res, a.out_bf16, a.residual, a.Cout, a.T, a.residual_stride, cols, 32))) {
     *why = "tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -552,25 +540,14 @@ cudaError_t go_split(const SplitArgs& p, int S, unsigned ctiles, unsigned rtiles
   constexpr size_t bytes = split_smem<N>();
   cudaError_t e = allow_smem<split_kernel<N, TO>>(bytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctiles * S, rtiles);
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, split_kernel<N, TO>, p, S);
+  return launch_cluster(split_kernel<N, TO>, dim3(ctiles * S, rtiles), kSplitThreads, bytes, S, stream, p, S);
 }
 
 template <int N>
 cudaError_t launch_split(const LinearArgs& a, int S, cudaStream_t stream, const char** why) {
   SplitArgs p{};
-  if (!encode(&p.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, N) ||
-      !encode(&p.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, 128)) {
+  if (!encode_rows(&p.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, N) ||
+      !encode_rows(&p.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, 128)) {
     *why = "tensor map encoding failed";
     return cudaErrorInvalidValue;
   }
@@ -596,6 +573,18 @@ cudaError_t launch_split(const LinearArgs& a, int S, cudaStream_t stream, const 
 }
 
 }  // namespace lintc
+
+bool encode_rows(CUtensorMap* m, bool bf16, const void* base, long long cols, long long rows, long long stride, int box_cols,
+            int box_rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                    const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
   using namespace lintc;
