@@ -141,7 +141,8 @@ cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, int threads, si
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
 }
 
-// Tensor map of a [rows][cols] tensor whose rows are `stride` elements apart; 128B-swizzled boxes.
+// Tensor map of a [rows][cols] tensor whose rows are `stride` elements apart; boxes of 128 (64) bytes a
+// row, 128B- (64B-)swizzled.
 bool encode_rows(CUtensorMap* m, bool bf16, const void* base, long long cols, long long rows, long long stride,
                  int box_cols, int box_rows);
 

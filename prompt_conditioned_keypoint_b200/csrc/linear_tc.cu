@@ -4,11 +4,11 @@
 // fills (128B-swizzled K-major tiles, zeros past every edge) and accumulate in
 // fp32 in tensor memory.
 //
-//   rows_kernel    many rows: 128 rows x 256 columns per tile, rows on the lanes.
+//   rows_kernel    many rows: 128 rows x 256 (192, 128) columns per tile, rows on the lanes.
 //                  One CTA per SM walks over the tiles; two accumulators, so that
 //                  the next tile's products run under this tile's epilogue.
 //   split_kernel   few rows: 128 columns (the weights, which are the large operand,
-//                  on the lanes) x N <= 128 rows per tile; a cluster of S CTAs
+//                  on the lanes) x N <= 64 rows per tile; a cluster of S CTAs
 //                  shares a tile's channels, and their partial sums meet in
 //                  shared memory (rank order, so the result is always the same).
 //
@@ -33,17 +33,18 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {   // fp32 accumulator, b
 // ---------------------------------------------------------------------------
 // Many rows
 // ---------------------------------------------------------------------------
-constexpr int kM = 128, kN = 256;
-constexpr int kABytes = kM * 128, kBBytes = kN * 128, kStageBytes = kABytes + kBBytes;
+constexpr int kM = 128, kABytes = kM * 128;
 constexpr int kEpiWarps = 8, kWarps = 2 + kEpiWarps, kThreads = 32 * kWarps;
-constexpr int kBufBytes = 4096;                    // 32 rows x 128 bytes of output (or residual), per epilogue warp
+constexpr int kBufBytes = 2048;                    // 32 rows x 64 bytes of output (or residual); two per epilogue warp
+constexpr int kMaxStages = 6;
 
-// With a residual a warp keeps two buffers (one being loaded while the other is
-// worked on) and the ring gives up a stage for them.
-template <bool RES>
-struct Ring {
-  static constexpr int kStages = RES ? 3 : 4, kBufs = RES ? 2 : 1;
-  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * kBufs * kBufBytes + 512;
+// NT: columns of a tile.
+template <int NT>
+struct Tile {
+  static constexpr int kBBytes = NT * 128, kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = NT == 128 ? 6 : 4;
+  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStageBytes) + kEpiWarps * 2 * kBufBytes + 512;
+  static_assert(kStages <= kMaxStages && kSmem <= 227 * 1024, "ring");
 };
 
 struct RowsArgs {
@@ -56,21 +57,22 @@ struct RowsArgs {
 };
 
 struct RowsCtl {
-  uint64_t full[4], empty[4], accfull[2], accempty[2], res[kEpiWarps][2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], res[kEpiWarps][2], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(sizeof(RowsCtl) <= 512, "control block");
 
-template <bool F32OUT, bool RES>
+template <int NT, bool F32OUT, bool RES>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ RowsArgs a) {
-  using R = Ring<RES>;
+  using R = Tile<NT>;
+  constexpr int kStageBytes = R::kStageBytes, kStages = R::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* bufs = smem + R::kStages * kStageBytes;
-  RowsCtl* ctl = reinterpret_cast<RowsCtl*>(bufs + kEpiWarps * R::kBufs * kBufBytes);
+  uint8_t* bufs = smem + kStages * kStageBytes;
+  RowsCtl* ctl = reinterpret_cast<RowsCtl*>(bufs + kEpiWarps * 2 * kBufBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ncol = (a.Cout + kN - 1) / kN;
+  const int ncol = (a.Cout + NT - 1) / NT;
   const long long ntiles = static_cast<long long>((a.T + kM - 1) / kM) * ncol;
   const int nk = (a.Cin + kChunk - 1) / kChunk;
   const int flush = F32OUT ? kFlush : nk;            // stages per accumulator
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
   };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < R::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
@@ -109,10 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
       uint32_t it = 0;
       bool ok = true;
       for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-        const int t0 = static_cast<int>(tile / ncol) * kM, n0 = static_cast<int>(tile % ncol) * kN;
+        const int t0 = static_cast<int>(tile / ncol) * kM, n0 = static_cast<int>(tile % ncol) * NT;
         for (int k = 0; k < nk; ++k, ++it) {
-          const uint32_t s = it % R::kStages, ph = (it / R::kStages) & 1;
-          if (it >= R::kStages && !mbar_wait_bounded(&ctl->empty[s], ph ^ 1, lim, abortp)) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+          if (it >= kStages && !mbar_wait_bounded(&ctl->empty[s], ph ^ 1, lim, abortp)) {
             give_up();
             ok = false;
             break;
@@ -122,59 +124,59 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
           tma_load_2d(smem + s * kStageBytes + kABytes, &a.w, &ctl->full[s], k * kChunk, n0);
         }
       }
-      for (uint32_t k = 0; k < R::kStages && k < it; ++k) {
+      for (uint32_t k = 0; k < kStages && k < it; ++k) {
         const uint32_t last = it - 1 - k;
-        if (!mbar_wait_drain(&ctl->full[last % R::kStages], (last / R::kStages) & 1, lim)) atomicOr(a.err, kErrTimeout);
+        if (!mbar_wait_drain(&ctl->full[last % kStages], (last / kStages) & 1, lim)) atomicOr(a.err, kErrTimeout);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA (one thread)
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(kN);
-      const uint64_t adesc = umma_desc_sw128(smem_u32(smem)), bdesc = umma_desc_sw128(smem_u32(smem) + kABytes);
-      uint32_t it = 0, acc = 0;
-      bool ok = true;
-      for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-        for (int k = 0; k < nk; ++k, ++it) {
-          const uint32_t s = it % R::kStages, ph = (it / R::kStages) & 1;
-          const uint32_t buf = acc & 1;
-          const bool fresh = k % flush == 0;
-          if (fresh && acc >= 2 && !mbar_wait_bounded(&ctl->accempty[buf], ((acc >> 1) & 1) ^ 1, lim, abortp)) ok = false;
-          if (ok && !mbar_wait_bounded(&ctl->full[s], ph, lim, abortp)) ok = false;
-          if (!ok) {
-            give_up();
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t off = static_cast<uint64_t>((s * kStageBytes + kk * 32) >> 4);
-            umma_ss_f16(tmem + buf * kN, adesc + off, bdesc + off, idesc, (!fresh || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(&ctl->empty[s]);
-          if (k % flush == flush - 1 || k == nk - 1) {
-            umma_commit(&ctl->accfull[buf]);
-            ++acc;
-          }
+    // ---------------------------------------------------------------- MMA
+    // The warp stays converged and one elected lane issues: descriptors then live in
+    // uniform registers (a lone thread takes some 230 clocks per product).
+    const uint32_t idesc = idesc_bf16(NT);
+    const uint64_t adesc = umma_desc_sw128(smem_u32(smem)), bdesc = umma_desc_sw128(smem_u32(smem) + kABytes);
+    uint32_t it = 0, acc = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw) && ok;
+      return ok;
+    };
+    for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+      for (int k = 0; k < nk; ++k, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+        const uint32_t buf = acc & 1;
+        const bool fresh = k % flush == 0;
+        if (fresh && acc >= 2 && !wait(&ctl->accempty[buf], ((acc >> 1) & 1) ^ 1)) break;
+        if (!wait(&ctl->full[s], ph)) break;
+        tc_fence_after();
+        const uint64_t off = static_cast<uint64_t>((s * kStageBytes) >> 4);
+        umma_ss_f16_x4_elect(tmem + buf * 256, adesc + off, bdesc + off, idesc, fresh ? 0u : 1u);
+        umma_commit_elect(&ctl->empty[s]);
+        if (k % flush == flush - 1 || k == nk - 1) {
+          umma_commit_elect(&ctl->accfull[buf]);
+          ++acc;
         }
       }
-      if (it > 0) {
-        umma_commit(&ctl->drain);
-        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
-      }
+    }
+    if (!ok && lane == 0) give_up();
+    if (it > 0) {                                     // what was issued ends before the CTA does
+      umma_commit_elect(&ctl->drain);
+      if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
     }
     __syncwarp();
   } else {
-    // ---------------------------------------------------------------- epilogue: 32 rows x 128 columns per warp
+    // ---------------------------------------------------------------- epilogue: 32 rows x NT / 2 columns per warp
     const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
-    uint8_t* mybuf = bufs + ew * R::kBufs * kBufBytes;
-    constexpr int kCols = F32OUT ? 32 : 64;          // columns of one 128-byte buffer row
-    constexpr int kPieces = 128 / kCols;
+    uint8_t* mybuf = bufs + ew * 2 * kBufBytes;
+    constexpr int kHalf = NT / 2;
+    constexpr int kCols = F32OUT ? 16 : 32;          // columns of one 64-byte buffer row
+    constexpr int kPieces = kHalf / kCols;
     uint32_t acc = 0, piece = 0;                     // accumulators read, output pieces written
     bool ok = true;
     for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-      const int t0 = static_cast<int>(tile / ncol) * kM + 32 * q, n0 = static_cast<int>(tile % ncol) * kN + 128 * half;
+      const int t0 = static_cast<int>(tile / ncol) * kM + 32 * q, n0 = static_cast<int>(tile % ncol) * NT + kHalf * half;
       const int pieces = (t0 < a.T && n0 < a.Cout) ? min(kPieces, (a.Cout - n0 + kCols - 1) / kCols) : 0;
       // the residual of the first piece is on its way while the products run
       if (RES && pieces > 0 && lane == 0) {
@@ -182,10 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         mbar_arrive_expect_tx(&ctl->res[ew][piece & 1], kBufBytes);
         tma_load_2d(mybuf + (piece & 1) * kBufBytes, &a.res, &ctl->res[ew][piece & 1], n0, t0);
       }
-      float v[128];
+      float v[kHalf];
       if (F32OUT) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) v[j] = 0.f;
+        for (int j = 0; j < kHalf; ++j) v[j] = 0.f;
       }
       for (int k0 = 0; k0 < nk; k0 += flush, ++acc) {
         const uint32_t buf = acc & 1;
@@ -195,9 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
           break;
         }
         tc_fence_after();
-        const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kN + 128 * half;
+        const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * 256 + kHalf * half;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
+        for (int g = 0; g < kHalf / 16; ++g) {
           uint32_t r[16];
           tmem_ld_32x32b_x16(src + 16 * g, r);
           tmem_wait_ld_regs(r);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         if (p >= pieces || !ok) continue;
-        uint8_t* buf = mybuf + (RES ? (piece & 1) : 0) * kBufBytes;
+        uint8_t* buf = mybuf + (piece & 1) * kBufBytes;
         const int c0 = n0 + p * kCols;
         if (RES) {
           if (p + 1 < pieces && lane == 0) {          // the next piece's residual
@@ -243,14 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             continue;
           }
         } else {
-          if (lane == 0) tma_store_wait_read<0>();
+          if (lane == 0) tma_store_wait_read<1>();
           __syncwarp();
         }
-        const uint32_t row = smem_u32(buf) + lane * 128u;
+        const uint32_t row = smem_u32(buf) + lane * 64u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {                 // 16-byte vectors of the 128-byte row
+        for (int j = 0; j < 4; ++j) {                 // 16-byte vectors of the 64-byte row, 64B-swizzled
           constexpr int kE = F32OUT ? 4 : 8;
-          const uint32_t at = row + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4);
+          const uint32_t at = row + ((static_cast<uint32_t>(j) ^ ((lane >> 1) & 3u)) << 4);
           const int c = c0 + j * kE;
           float y[kE];
 #pragma unroll
@@ -319,7 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
-constexpr int kSplitThreads = 256, kSplitStages = 6;
+constexpr int kSplitThreads = 256;
+// Stages of 64 channels: as many as let two CTAs share an SM (one CTA's latencies under the
+// other's), six at most.
+template <int N>
+constexpr int kSplitStagesOf = N <= 16 ? 6 : N <= 32 ? 5 : 4;
 constexpr int kWBytes = 128 * 128;                 // a stage's weights: 128 columns x 64 channels
 
 struct SplitArgs {
@@ -336,21 +342,21 @@ struct SplitArgs {
 };
 
 struct SplitCtl {
-  uint64_t full[kSplitStages], empty[kSplitStages], accfull, drain;
+  uint64_t full[6], empty[6], accfull, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 template <int N>
 constexpr size_t split_smem() {
-  return 1024 + kSplitStages * static_cast<size_t>(kWBytes + N * 128) + sizeof(SplitCtl);
+  return 1024 + kSplitStagesOf<N> * static_cast<size_t>(kWBytes + N * 128) + sizeof(SplitCtl);
 }
 
 template <int N, typename TO>
-__global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_constant__ SplitArgs a, int S) {
+__global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_constant__ SplitArgs a, int S) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kBytes = kWBytes + N * 128;
+  constexpr int kBytes = kWBytes + N * 128, kSplitStages = kSplitStagesOf<N>;
   static_assert(N * 512 <= kSplitStages * kBytes, "the partial sums take the ring's place");
   SplitCtl* ctl = reinterpret_cast<SplitCtl*>(smem + kSplitStages * kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -404,32 +410,28 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(N);
-      const uint64_t wdesc = umma_desc_sw128(smem_u32(smem)), xdesc = umma_desc_sw128(smem_u32(smem) + kWBytes);
-      bool ok = true;
-      uint32_t it = 0;
-      for (; it < static_cast<uint32_t>(nk); ++it) {
-        const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
-        if (!mbar_wait_bounded(&ctl->full[s], ph, lim, abortp)) {
-          ctl->abort_flag = 1;
-          atomicOr(a.err, kErrTimeout);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t off = static_cast<uint64_t>((s * kBytes + kk * 32) >> 4);
-          umma_ss_f16(tmem + (it / per) * N, wdesc + off, xdesc + off, idesc, (it % per || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(&ctl->empty[s]);
-      }
-      if (ok) umma_commit(&ctl->accfull);
-      if (it > 0) {
-        umma_commit(&ctl->drain);
-        if (!mbar_wait_drain(&ctl->drain, 0, lim)) atomicOr(a.err, kErrTimeout);
-      }
+    const uint32_t idesc = idesc_bf16(N);
+    const uint64_t wdesc = umma_desc_sw128(smem_u32(smem)), xdesc = umma_desc_sw128(smem_u32(smem) + kWBytes);
+    bool ok = true;
+    uint32_t it = 0;
+    for (; it < static_cast<uint32_t>(nk); ++it) {
+      const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
+      const bool okw = mbar_wait_bounded(&ctl->full[s], ph, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>((s * kBytes) >> 4);
+      umma_ss_f16_x4_elect(tmem + (it / per) * N, wdesc + off, xdesc + off, idesc, it % per ? 1u : 0u);
+      umma_commit_elect(&ctl->empty[s]);
+    }
+    if (ok) umma_commit_elect(&ctl->accfull);
+    if (!ok && lane == 0) {
+      ctl->abort_flag = 1;
+      atomicOr(a.err, kErrTimeout);
+    }
+    if (it > 0) {                                     // what was issued ends before the CTA does
+      umma_commit_elect(&ctl->drain);
+      if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
     }
     __syncwarp();
   }
@@ -503,19 +505,20 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-template <bool F32OUT, bool RES>
+template <int NT, bool F32OUT, bool RES>
 cudaError_t go_rows(const RowsArgs& r, unsigned grid, cudaStream_t stream) {
-  cudaError_t e = allow_smem<rows_kernel<F32OUT, RES>>(Ring<RES>::kSmem);
+  cudaError_t e = allow_smem<rows_kernel<NT, F32OUT, RES>>(Tile<NT>::kSmem);
   if (e != cudaSuccess) return e;
-  rows_kernel<F32OUT, RES><<<grid, kThreads, Ring<RES>::kSmem, stream>>>(r);
+  rows_kernel<NT, F32OUT, RES><<<grid, kThreads, Tile<NT>::kSmem, stream>>>(r);
   return cudaGetLastError();
 }
 
+template <int NT>
 cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
   RowsArgs r{};
-  const int cols = a.out_bf16 ? 64 : 32;
+  const int cols = a.out_bf16 ? 32 : 16;             // 64 bytes
   if (!encode_rows(&r.x, true, a.x, a.Cin, a.T, a.x_stride, kChunk, kM) ||
-      !encode_rows(&r.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, kN) ||
+      !encode_rows(&r.w, true, a.weight, a.Cin, a.Cout, a.Cin, kChunk, NT) ||
       !encode_rows(&r.out, a.out_bf16, a.out, a.Cout, a.T, a.out_stride, cols, 32) ||
       (a.residual && !encode_rows(&r.res, a.out_bf16, a.residual, a.Cout, a.T, a.residual_stride, cols, 32))) {
     *why = "tensor map encoding failed";
@@ -529,10 +532,10 @@ cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, c
   r.act = a.act;
   r.err = a.err;
   r.wait_limit_ns = a.wait_limit_ns;
-  const long long tiles = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + kN - 1) / kN);
+  const long long tiles = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + NT - 1) / NT);
   const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
-  if (a.out_bf16) return a.residual ? go_rows<false, true>(r, grid, stream) : go_rows<false, false>(r, grid, stream);
-  return a.residual ? go_rows<true, true>(r, grid, stream) : go_rows<true, false>(r, grid, stream);
+  if (a.out_bf16) return a.residual ? go_rows<NT, false, true>(r, grid, stream) : go_rows<NT, false, false>(r, grid, stream);
+  return a.residual ? go_rows<NT, true, true>(r, grid, stream) : go_rows<NT, true, false>(r, grid, stream);
 }
 
 template <int N, typename TO>
@@ -582,28 +585,43 @@ bool encode_rows(CUtensorMap* m, bool bf16, const void* base, long long cols, lo
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
   return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                     const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                    box_cols * (bf16 ? 2 : 4) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why) {
   using namespace lintc;
-  const long long big = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + kN - 1) / kN);
-  if (big > num_sms / 2) return launch_rows(a, num_sms, stream, why);
-  const int N = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
-  const long long tiles = (static_cast<long long>(a.T) + N - 1) / N * ((a.Cout + 127) / 128);
+  const long long rtiles = (static_cast<long long>(a.T) + kM - 1) / kM;
+  auto ctiles = [&](int n) { return static_cast<long long>((a.Cout + n - 1) / n); };
+  if (2 * rtiles * ctiles(128) > num_sms) {
+    // The width whose waves of tiles cost least. A wave takes 1.00 : 0.80 : 0.63 of the time
+    // for 256 : 192 : 128 columns (36864 x 1280 -> 5120: 363, 396, 460 us; 5120 x 1024 -> 1024,
+    // where 256 leaves its second wave nearly empty: 19.3, 17.5, 18.2 us).
+    auto cost = [&](int n, int weight) { return (rtiles * ctiles(n) + num_sms - 1) / num_sms * weight; };
+    const long long c256 = cost(256, 100), c192 = cost(192, 80), c128 = cost(128, 63);
+    if (c256 <= c192 && c256 <= c128) return launch_rows<256>(a, num_sms, stream, why);
+    return c192 <= c128 ? launch_rows<192>(a, num_sms, stream, why) : launch_rows<128>(a, num_sms, stream, why);
+  }
+  // Fewer than half as many tiles as SMs: the channels are split too, while that keeps to about
+  // one CTA per SM and leaves each CTA some stages (80 x 4096 -> 1024: 21.1, 14.2, 10.2, 9.7 us
+  // with 1, 2, 4, 8; 80 x 1024 -> 1024: 9.8, 8.5, 7.3, 7.8 us; 256 x 1024 -> 1024, where 8 would
+  // be two CTAs per SM: 7.8 us with 4, 9.8 with 8; one tile of 128 columns instead: 10.1 us).
   const int nk = (a.Cin + kChunk - 1) / kChunk;
-  int S = 1;
-  while (S < 8 && tiles * S * 2 <= num_sms && nk >= 4 * S) S *= 2;
+  int N = a.T <= 32 ? 16 : a.T <= 64 ? 32 : 64, S;
+  for (;; N /= 2) {
+    const long long tiles = (static_cast<long long>(a.T) + N - 1) / N * ctiles(128);
+    S = 1;
+    while (S < 8 && tiles * 2 * S <= num_sms + num_sms / 8 && nk >= (tiles * 4 * S <= num_sms ? 4 : 8) * S) S *= 2;
+    // an fp32 output wants at most 512 channels per accumulator: narrower tiles leave room for more of them
+    if (a.out_bf16 || N == 16 || (nk + S - 1) / S <= 512 / N * kFlush) break;
+  }
   switch (N) {
     case 16:
       return launch_split<16>(a, S, stream, why);
     case 32:
       return launch_split<32>(a, S, stream, why);
-    case 64:
-      return launch_split<64>(a, S, stream, why);
     default:
-      return launch_split<128>(a, S, stream, why);
+      return launch_split<64>(a, S, stream, why);
   }
 }
 
