@@ -209,12 +209,12 @@ def gkd_heatmap_contract_first(feat, fdt, B, h, w, C, up, kern, kern_batch_strid
 
 def gkd_heads(x) -> GkdHeads | None:
     """The gkd_heads view of a tensor [B][rows][heads][D] (any strides, last axis contiguous); views and None pass."""
-    if x is None or isinstance(x, GkdHeads):
+    if x is None or x.__class__ is GkdHeads:
         return x
     strides = x.stride()
-    if len(strides) != 4 or (strides[3] != 1 and x.shape[3] > 1):
+    if len(strides) != 4 or (strides[3] != 1 and x.size(3) > 1):
         raise GkdError(GKD_ERR_SHAPE, "gkd_heads", "a view is [B][rows][heads][D] with contiguous D")
-    return GkdHeads(x.data_ptr(), strides[0], strides[1], strides[2], x.shape[2])
+    return GkdHeads(x.data_ptr(), strides[0], strides[1], strides[2], x.size(2))
 
 
 def gkd_linear(x, dt, T, Cin, x_stride, weight, Cout, bias, act, scale, residual, residual_stride, out, out_dt,

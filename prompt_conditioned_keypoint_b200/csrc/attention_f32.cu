@@ -1,12 +1,14 @@
 // gkd_attention on the fp32 units, fp32: out = softmax(scale q k^T) v under a key mask.
 //
 // One CTA per (batch, head, 64 query rows). Keys come 64 at a time: a thread has
-// 4 rows x 8 keys of the scores and 4 rows x (D / 8) columns of the output, with
+// 4 rows (16 apart) x 8 keys (8 apart) of the scores and 4 rows x (D / 8) columns of the output, with
 // the running maximum and sum of its rows (the eight threads of a row group agree
 // on them by shuffles). Scores are kept in units of log 2. Key tiles that the
 // mask or the diagonal leaves empty are skipped; hidden keys and values are
 // replaced by zeros on their way into shared memory, so what they hold never
 // meets a product.
+#include <type_traits>
+
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
@@ -14,16 +16,18 @@ namespace gkd {
 namespace att {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+constexpr int kPitch = 72;   // floats between rows of weights: a warp's 4 rows x 8 keys fall on 32 banks
 
 template <int DC>   // DC: head columns in units of 32, rounded up
-__global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_constant__ AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) attention_f32_kernel(const __grid_constant__ AttentionArgs a) {
   extern __shared__ float sm[];
   constexpr int DP = 32 * DC + 4;
   float* qs = sm;
   float* ks = qs + kRows * DP;
   float* vs = ks + kKeys * DP;
-  float* ps = vs + kKeys * DP;                       // [64][68]
+  float* ps = vs + kKeys * DP;                       // [64][kPitch]
   __shared__ uint8_t ok[kKeys];
+  __shared__ uint32_t words[2];
   const int tid = threadIdx.x, rg = tid >> 3, cg = tid & 7;
   const int ntiles = (a.Tq + kRows - 1) / kRows;
   const int tile = blockIdx.x % ntiles;
@@ -37,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
   const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
   const int nq4 = a.D / 4;
   const float qscale = a.scale * 1.4426950408889634f;
+#pragma unroll 8
   for (int e = tid; e < kRows * 8 * DC; e += kThreads) {
     const int r = e / (8 * DC), c = e % (8 * DC);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -59,11 +64,19 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
     if (tid < kKeys) {
       mine = k0 + tid < a.Tk && (!mask || mask[k0 + tid] != 0);
     }
-    const int any = __syncthreads_or(mine);
-    if (!any) continue;
+    // keys up to the last visible one, in eights
+    const uint32_t bits = __ballot_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0 && tid < kKeys) words[tid >> 5] = bits;
     if (tid < kKeys) ok[tid] = mine;
     __syncthreads();
-    for (int e = tid; e < kKeys * 8 * DC; e += kThreads) {
+    const uint32_t w0 = words[0], w1 = words[1];
+    if (!(w0 | w1)) {
+      __syncthreads();
+      continue;
+    }
+    const int groups = w1 ? 8 - (__clz(w1) >> 3) : 4 - (__clz(w0) >> 3);
+#pragma unroll 4
+    for (int e = tid; e < 8 * groups * 8 * DC; e += kThreads) {
       const int r = e / (8 * DC), c = e % (8 * DC);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (ok[r] && c < nq4) {
@@ -79,21 +92,28 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
-    for (int c = 0; c < nq4; ++c) {
-      float4 qv[4], kv[8];
+    auto dots = [&](auto half) {                                  // of the first 4 or all 8 groups of keys
+      constexpr int kGroups = decltype(half)::value ? 4 : 8;
+      for (int c = 0; c < nq4; ++c) {
+        float4 qv[4], kv[kGroups];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (4 * rg + i) * DP + 4 * c);
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (rg + 16 * i) * DP + 4 * c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (cg + 8 * j) * DP + 4 * c);
+        for (int j = 0; j < kGroups; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (cg + 8 * j) * DP + 4 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
-    }
+          for (int j = 0; j < kGroups; ++j)
+            s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
+      }
+    };
+    if (groups <= 4)
+      dots(std::true_type{});
+    else
+      dots(std::false_type{});
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long row = r0 + 4 * rg + i;
+      const long long row = r0 + rg + 16 * i;
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -105,13 +125,13 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
       for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float mn = fmaxf(m[i], top);
       const float base = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: every weight is 0
-      const float f = exp2f(m[i] - base);
+      const float f = ex2_approx(m[i] - base);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float p = exp2f(s[i][j] - base);
+        const float p = ex2_approx(s[i][j] - base);
         sum += p;
-        ps[(4 * rg + i) * 68 + cg + 8 * j] = p;
+        ps[(rg + 16 * i) * kPitch + cg + 8 * j] = p;
       }
 #pragma unroll
       for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -121,11 +141,11 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
       for (int c = 0; c < 4 * DC; ++c) acc[i][c] *= f;
     }
     __syncwarp();                                                 // a row's weights come from its own warp
-#pragma unroll 4
-    for (int j4 = 0; j4 < kKeys / 4; ++j4) {
+#pragma unroll 2
+    for (int j4 = 0; j4 < 2 * groups; ++j4) {
       float4 pv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (4 * rg + i) * 68 + 4 * j4);
+      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (rg + 16 * i) * kPitch + 4 * j4);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
@@ -146,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long row = r0 + 4 * rg + i;
+    const long long row = r0 + rg + 16 * i;
     if (row >= a.Tq) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
@@ -160,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) attention_f32_kernel(const __grid_co
 
 template <int DC>
 cudaError_t go(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * 68);
+  constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * kPitch);
   cudaError_t e = allow_smem<attention_f32_kernel<DC>>(bytes);
   if (e != cudaSuccess) return e;
   attention_f32_kernel<DC><<<grid, kThreads, bytes, stream>>>(a);

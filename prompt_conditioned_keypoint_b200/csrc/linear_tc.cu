@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
       const int t0 = static_cast<int>(tile / ncol) * kM + 32 * q, n0 = static_cast<int>(tile % ncol) * NT + kHalf * half;
       const int pieces = (t0 < a.T && n0 < a.Cout) ? min(kPieces, (a.Cout - n0 + kCols - 1) / kCols) : 0;
-      // the residual of the first piece is on its way while the products run
+      // the residual is on its way while the products run: to L2, the first piece to its buffer
+      if (RES && lane > 0 && lane < pieces) tma_prefetch_2d(&a.res, n0 + lane * kCols, t0);
       if (RES && pieces > 0 && lane == 0) {
         tma_store_wait_read<1>();
         mbar_arrive_expect_tx(&ctl->res[ew][piece & 1], kBufBytes);

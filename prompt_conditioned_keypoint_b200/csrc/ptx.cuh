@@ -170,6 +170,12 @@ __device__ __forceinline__ void tma_load_5d(void* smem_dst, const void* tmap, ui
       : "memory");
 }
 
+// Brings a box into L2 (no completion to wait for).
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+               ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1) : "memory");
+}
+
 // TMA store of a tile from shared memory (the tensor's extents clip it). The
 // calling thread's group commits it; wait_read<N> returns when all but the last N
 // groups have read their shared memory, wait<N> when they are complete.
