@@ -226,6 +226,31 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         if (p >= pieces || !ok) continue;
         uint8_t* buf = mybuf + (piece & 1) * kBufBytes;
         const int c0 = n0 + p * kCols;
+        // Bias and activation for the whole piece at once, without branches per vector: columns
+        // past Cout (a multiple of 8) take the last ones' values and are clipped by the store.
+        float(&y)[kCols] = reinterpret_cast<float(&)[kCols]>(v[p * kCols]);
+        auto column = [&](int j) { return min(c0 + 4 * j, a.Cout - 4); };
+        if (a.bias) {
+#pragma unroll
+          for (int j = 0; j < kCols / 4; ++j) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + column(j)));
+            y[4 * j] += b.x;
+            y[4 * j + 1] += b.y;
+            y[4 * j + 2] += b.z;
+            y[4 * j + 3] += b.w;
+          }
+        }
+        activate(y, a.act);
+        if (a.scale) {
+#pragma unroll
+          for (int j = 0; j < kCols / 4; ++j) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(a.scale + column(j)));
+            y[4 * j] *= b.x;
+            y[4 * j + 1] *= b.y;
+            y[4 * j + 2] *= b.z;
+            y[4 * j + 3] *= b.w;
+          }
+        }
         if (RES) {
           if (p + 1 < pieces && lane == 0) {          // the next piece's residual
             tma_store_wait_read<0>();
@@ -254,31 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         for (int j = 0; j < 4; ++j) {                 // 16-byte vectors of the 64-byte row, 64B-swizzled
           constexpr int kE = F32OUT ? 4 : 8;
           const uint32_t at = row + ((static_cast<uint32_t>(j) ^ ((lane >> 1) & 3u)) << 4);
-          const int c = c0 + j * kE;
-          float y[kE];
-#pragma unroll
-          for (int e = 0; e < kE; ++e) y[e] = v[p * kCols + j * kE + e];
-          if (c < a.Cout) {                           // Cout is a multiple of 8: a vector is in or out
-#pragma unroll
-            for (int e = 0; e < kE; e += 4) {
-              const float4 b = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              y[e] += b.x;
-              y[e + 1] += b.y;
-              y[e + 2] += b.z;
-              y[e + 3] += b.w;
-            }
-            activate(y, a.act);
-            if (a.scale) {
-#pragma unroll
-              for (int e = 0; e < kE; e += 4) {
-                const float4 b = __ldg(reinterpret_cast<const float4*>(a.scale + c + e));
-                y[e] *= b.x;
-                y[e + 1] *= b.y;
-                y[e + 2] *= b.z;
-                y[e + 3] *= b.w;
-              }
-            }
-          }
           uint32_t o[4];
           if (RES) {
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -286,16 +286,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (F32OUT) {
-                y[e] += __uint_as_float(o[e]);
+                y[kE * j + e] += __uint_as_float(o[e]);
               } else {
-                y[2 * e % kE] += bf16_lo(o[e]);
-                y[(2 * e + 1) % kE] += bf16_hi(o[e]);
+                y[(kE * j + 2 * e) % kCols] += bf16_lo(o[e]);
+                y[(kE * j + 2 * e + 1) % kCols] += bf16_hi(o[e]);
               }
             }
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = F32OUT ? __float_as_uint(y[e]) : pack_bf16x2(y[2 * e % kE], y[(2 * e + 1) % kE]);
+            o[e] = F32OUT ? __float_as_uint(y[kE * j + e])
+                          : pack_bf16x2(y[(kE * j + 2 * e) % kCols], y[(kE * j + 2 * e + 1) % kCols]);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                        ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
         }
