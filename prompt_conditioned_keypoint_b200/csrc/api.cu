@@ -759,7 +759,7 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   const char* why = "";
   const cudaError_t e = dt == GKD_BF16
                             ? gkd::launch_attention_tc(a, ds->num_sms, static_cast<cudaStream_t>(stream), &why)
-                            : gkd::launch_attention_f32(a, static_cast<cudaStream_t>(stream));
+                            : gkd::launch_attention_f32(a, ds->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "attention: %s", why);
   return launched(e, "attention");
 }

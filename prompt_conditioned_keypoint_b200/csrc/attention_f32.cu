@@ -6,7 +6,7 @@
 // on them by shuffles). Scores are kept in units of log 2. Key tiles that the
 // mask or the diagonal leaves empty are skipped; hidden keys and values are
 // replaced by zeros on their way into shared memory, so what they hold never
-// meets a product.
+// meets a product. Few query tiles: a cluster of S CTAs shares the key tiles of one.
 #include <type_traits>
 
 #include "blocks_common.cuh"
@@ -19,7 +19,7 @@ constexpr int kRows = 64, kKeys = 64, kThreads = 128;
 constexpr int kPitch = 72;   // floats between rows of weights: a warp's 4 rows x 8 keys fall on 32 banks
 
 template <int DC>   // DC: head columns in units of 32, rounded up
-__global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) attention_f32_kernel(const __grid_constant__ AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) attention_f32_kernel(const __grid_constant__ AttentionArgs a, int S) {
   extern __shared__ float sm[];
   constexpr int DP = 32 * DC + 4;
   float* qs = sm;
@@ -30,8 +30,9 @@ __global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) atten
   __shared__ uint32_t words[2];
   const int tid = threadIdx.x, rg = tid >> 3, cg = tid & 7;
   const int ntiles = (a.Tq + kRows - 1) / kRows;
-  const int tile = blockIdx.x % ntiles;
-  const int bh = blockIdx.x / ntiles, h = bh % a.q.heads, b = bh / a.q.heads;
+  const int rank = blockIdx.x % S, work = blockIdx.x / S;         // = the rank in the cluster, the query tile
+  const int tile = work % ntiles;
+  const int bh = work / ntiles, h = bh % a.q.heads, b = bh / a.q.heads;
   const int hk = h / (a.q.heads / a.k.heads);
   const int r0 = tile * kRows;
   const float* q = static_cast<const float*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
@@ -59,7 +60,10 @@ __global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) atten
   const long long shift = static_cast<long long>(a.Tk) - a.Tq;   // causal: key j for row i iff j <= i + shift
   long long klast = a.Tk;
   if (a.causal) klast = min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift);
-  for (long long k0 = 0; k0 < klast; k0 += kKeys) {
+  // this CTA's share of the key tiles
+  const long long ktiles = klast > 0 ? (klast + kKeys - 1) / kKeys : 0;
+  const long long kend = min(klast, ktiles * (rank + 1) / S * kKeys);
+  for (long long k0 = ktiles * rank / S * kKeys; k0 < kend; k0 += kKeys) {
     bool mine = false;
     if (tid < kKeys) {
       mine = k0 + tid < a.Tk && (!mask || mask[k0 + tid] != 0);
@@ -164,43 +168,89 @@ __global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) atten
     }
     __syncthreads();
   }
+  if (S == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long row = r0 + rg + 16 * i;
+      if (row >= a.Tq) continue;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+      for (int d = 0; d < DC; ++d)
+        if (32 * d + 4 * cg < a.D)
+          store4(o + row * a.out.row_stride + 32 * d + 4 * cg,
+                 make_float4(acc[i][4 * d] * inv, acc[i][4 * d + 1] * inv, acc[i][4 * d + 2] * inv,
+                             acc[i][4 * d + 3] * inv));
+    }
+    return;
+  }
+  // The shares meet in shared memory, where the keys were: (O, m, l) of every row, in rank order.
+  float* ml = ps;                                                  // [64][2]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long row = r0 + rg + 16 * i;
-    if (row >= a.Tq) continue;
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    const int r = rg + 16 * i;
 #pragma unroll
     for (int d = 0; d < DC; ++d)
-      if (32 * d + 4 * cg < a.D)
-        store4(o + row * a.out.row_stride + 32 * d + 4 * cg,
-               make_float4(acc[i][4 * d] * inv, acc[i][4 * d + 1] * inv, acc[i][4 * d + 2] * inv,
-                           acc[i][4 * d + 3] * inv));
+      *reinterpret_cast<float4*>(ks + r * DP + 32 * d + 4 * cg) =
+          make_float4(acc[i][4 * d], acc[i][4 * d + 1], acc[i][4 * d + 2], acc[i][4 * d + 3]);
+    if (cg == 0) {
+      ml[2 * r] = m[i];
+      ml[2 * r + 1] = l[i];
+    }
   }
+  cluster_sync();
+  const uint32_t oo = smem_u32(ks), om = smem_u32(ml);
+  const int share = kRows / S;
+  for (int e = tid; e < share * nq4; e += kThreads) {
+    const int r = rank * share + e / nq4, c = e % nq4;
+    if (r0 + r >= a.Tq) continue;
+    float top = -INFINITY;
+    for (int s = 0; s < S; ++s) top = fmaxf(top, cluster_load1(cluster_map(om + 8 * r, s)));
+    float total = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < S; ++s) {
+      const float ms = cluster_load1(cluster_map(om + 8 * r, s));
+      if (ms == -INFINITY) continue;                               // a share without a key for this row
+      const float f = ex2_approx(ms - top);
+      const float4 v = cluster_load4(cluster_map(oo + 4 * (r * DP + 4 * c), s));
+      total = fmaf(f, cluster_load1(cluster_map(om + 8 * r + 4, s)), total);
+      y.x = fmaf(f, v.x, y.x);
+      y.y = fmaf(f, v.y, y.y);
+      y.z = fmaf(f, v.z, y.z);
+      y.w = fmaf(f, v.w, y.w);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    store4(o + (r0 + r) * a.out.row_stride + 4 * c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+  }
+  __syncwarp();
+  cluster_sync();                                                  // nobody leaves while its shared memory is read
 }
 
 template <int DC>
-cudaError_t go(const AttentionArgs& a, unsigned grid, cudaStream_t stream) {
+cudaError_t go(const AttentionArgs& a, unsigned work, int S, cudaStream_t stream) {
   constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * kPitch);
   cudaError_t e = allow_smem<attention_f32_kernel<DC>>(bytes);
   if (e != cudaSuccess) return e;
-  attention_f32_kernel<DC><<<grid, kThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_cluster(attention_f32_kernel<DC>, dim3(work * S), kThreads, bytes, S, stream, a, S);
 }
 
 }  // namespace att
 
-cudaError_t launch_attention_f32(const AttentionArgs& a, cudaStream_t stream) {
+cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
   const long long ntiles = (static_cast<long long>(a.Tq) + att::kRows - 1) / att::kRows;
-  const unsigned grid = static_cast<unsigned>(ntiles * a.q.heads * a.B);
+  const unsigned work = static_cast<unsigned>(ntiles * a.q.heads * a.B);
+  // few query tiles: a cluster shares the keys of one, while that keeps to two CTAs per SM
+  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + att::kKeys - 1) / att::kKeys);
+  int S = 1;
+  while (S < 8 && static_cast<long long>(work) * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
   switch ((a.D + 31) / 32) {
     case 1:
-      return att::go<1>(a, grid, stream);
+      return att::go<1>(a, work, S, stream);
     case 2:
-      return att::go<2>(a, grid, stream);
+      return att::go<2>(a, work, S, stream);
     case 3:
-      return att::go<3>(a, grid, stream);
+      return att::go<3>(a, work, S, stream);
     default:
-      return att::go<4>(a, grid, stream);
+      return att::go<4>(a, work, S, stream);
   }
 }
 

@@ -197,7 +197,7 @@ struct AttentionArgs {
   unsigned* err;
   unsigned long long wait_limit_ns;
 };
-cudaError_t launch_attention_f32(const AttentionArgs& a, cudaStream_t stream);
+cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16
 
 // cuTensorMapEncodeTiled resolved through the runtime's driver entry point.
