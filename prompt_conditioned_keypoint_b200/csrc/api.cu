@@ -757,9 +757,10 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
   const char* why = "";
-  const cudaError_t e = dt == GKD_BF16
-                            ? gkd::launch_attention_tc(a, ds->num_sms, static_cast<cudaStream_t>(stream), &why)
-                            : gkd::launch_attention_f32(a, ds->num_sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = Tk == 0          ? gkd::launch_attention_none(a, size, st)
+                        : dt == GKD_BF16 ? gkd::launch_attention_tc(a, ds->num_sms, st, &why)
+                                         : gkd::launch_attention_f32(a, ds->num_sms, st);
   if (e != cudaSuccess && why[0]) return fail(GKD_ERR_CUDA, "attention: %s", why);
   return launched(e, "attention");
 }

@@ -1,257 +1,479 @@
-// gkd_attention on the fp32 units, fp32: out = softmax(scale q k^T) v under a key mask.
+// gkd_attention for fp32 on the tensor cores: out = softmax(scale q k^T) v under a key
+// mask, with fp32 accuracy from bf16 products.
 //
-// One CTA per (batch, head, 64 query rows). Keys come 64 at a time: a thread has
-// 4 rows (16 apart) x 8 keys (8 apart) of the scores and 4 rows x (D / 8) columns of the output, with
-// the running maximum and sum of its rows (the eight threads of a row group agree
-// on them by shuffles). Scores are kept in units of log 2. Key tiles that the
-// mask or the diagonal leaves empty are skipped; hidden keys and values are
-// replaced by zeros on their way into shared memory, so what they hold never
-// meets a product. Few query tiles: a cluster of S CTAs shares the key tiles of one.
-#include <type_traits>
-
+// Every operand is taken as x = b0 + b1 + b2, b0 = bf16(x), b1 = bf16(x - b0), b2 =
+// bf16(x - b0 - b1): 24 bits. Of the nine products per term the six with i + j <= 2 are
+// formed (the others are below 2^-24 of the term), small ones first. bf16 planes rather
+// than TF32 pairs because the second product reads V across its rows, which 16-bit
+// operands allow in place. A fp32 unit version of this kernel (64 x 64 tiles in
+// shared memory) took 168 us for 64 x 160 padded rows of 16 heads of 64 and 1746 us
+// for 2 x 2309 rows of 20 heads.
+//
+// The tensor core truncates each step's sum, which over a long row of keys would drift
+// by 2^-23 per 32 keys: an output accumulator holds one tile of 64 keys, and the softmax
+// threads add the tiles up in fp32 registers, where rescaling them costs nothing either.
+//
+// A CTA has 128 query rows of one head, one CTA per SM, 16 warps:
+//   warp 0       decides which tiles of 64 keys are worth doing (mask and diagonal) and
+//                hands their key bits to the others through a small ring;
+//   warp 1       issues the products: the next tile's scores ahead of this tile's output;
+//   warps 4-7    softmax, one row per thread: maximum, weights, their three planes into
+//                tensor memory, and the last tile's output added up;
+//   warps 8-15   fetch K and V (the next tile's on their way meanwhile) and write their
+//                planes as 128B-swizzled tiles. Hidden keys and values become zeros.
+// Few query tiles: a cluster of S CTAs shares the key tiles of one and joins (O, m, l)
+// through shared memory in rank order.
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
 namespace gkd {
-namespace att {
+namespace att32 {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 128;
-constexpr int kPitch = 72;   // floats between rows of weights: a warp's 4 rows x 8 keys fall on 32 banks
+constexpr int kThreads = 512, kRows = 128, BN = 64, W = 2, kInfo = 4, kConvThreads = 256;
+// 512 threads have 128 registers each; the softmax warps hold a row of scores and one of outputs:
+// 64 + 240 + 2 x 104 <= 4 x 128.
+constexpr int kRegsIssue = 64, kRegsSoft = 240, kRegsConv = 104;
 
-template <int DC>   // DC: head columns in units of 32, rounded up
-__global__ void __launch_bounds__(kThreads, DC <= 2 ? 3 : DC == 3 ? 2 : 1) attention_f32_kernel(const __grid_constant__ AttentionArgs a, int S) {
-  extern __shared__ float sm[];
-  constexpr int DP = 32 * DC + 4;
-  float* qs = sm;
-  float* ks = qs + kRows * DP;
-  float* vs = ks + kKeys * DP;
-  float* ps = vs + kKeys * DP;                       // [64][kPitch]
-  __shared__ uint8_t ok[kKeys];
-  __shared__ uint32_t words[2];
-  const int tid = threadIdx.x, rg = tid >> 3, cg = tid & 7;
-  const int ntiles = (a.Tq + kRows - 1) / kRows;
-  const int rank = blockIdx.x % S, work = blockIdx.x / S;         // = the rank in the cluster, the query tile
-  const int tile = work % ntiles;
-  const int bh = work / ntiles, h = bh % a.q.heads, b = bh / a.q.heads;
-  const int hk = h / (a.q.heads / a.k.heads);
+struct Info {                                       // one key tile
+  int k0;                                           // first key, or -1: no more tiles
+  int plain;                                        // every key of the tile is visible to every row of the CTA
+  int words;                                        // 32-key groups up to the last visible key
+  uint32_t bits[W];                                 // keys that the mask and Tk leave
+};
+
+template <int DCH>
+struct Plan {
+  static constexpr int kStages = DCH == 1 ? 2 : 1;
+  static constexpr int kQPlane = kRows * 128 * DCH, kPlane = BN * 128 * DCH;        // bytes
+  static constexpr int kKvBytes = 3 * kPlane, kStageBytes = 2 * kKvBytes;           // K's planes, then V's
+  struct Ctl {
+    uint64_t qready, kready[kStages], kempty[kStages], vready[kStages], vempty[kStages];
+    uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready, odone, drain;
+    Info info[kInfo];
+    uint32_t tmem_base;
+    int abort_flag;
+    float m[kRows], l[kRows];                       // of the rows, for the other CTAs of the cluster
+  };
+  static constexpr size_t kSmem = 1024 + 3 * kQPlane + kStages * kStageBytes + sizeof(Ctl);
+};
+
+constexpr uint32_t kColP = 128, kColO = 256;        // scores at 0 and 64, P's planes of 32 columns, the tile's output
+
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t lbo) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Two values as their planes' bf16 pairs.
+__device__ __forceinline__ void planes(float x, float y, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = pack_bf16x2(x, y);
+    x -= bf16_lo(p[i]);
+    y -= bf16_hi(p[i]);
+  }
+}
+
+template <int DCH>
+__global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid_constant__ AttentionArgs a, int S) {
+  using P = Plan<DCH>;
+  constexpr int kStages = P::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kv = qs + 3 * P::kQPlane;
+  auto* ctl = reinterpret_cast<typename P::Ctl*>(kv + kStages * P::kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntiles = static_cast<int>((static_cast<long long>(a.Tq) + kRows - 1) / kRows);
+  const int rank = blockIdx.x % S, work = blockIdx.x / S;          // = the rank in the cluster, the query tile
+  const int tile = ntiles - 1 - work % ntiles;                     // with a diagonal the last rows have the most keys: first
+  const int bh = work / ntiles, h = bh % a.q.heads, b = bh / a.q.heads, hk = h / (a.q.heads / a.k.heads);
   const int r0 = tile * kRows;
-  const float* q = static_cast<const float*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
-  const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
-  const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
-  float* o = static_cast<float*>(a.out.data) + b * a.out.batch_stride + h * a.out.head_stride;
-  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
-  const int nq4 = a.D / 4;
-  const float qscale = a.scale * 1.4426950408889634f;
-#pragma unroll 8
-  for (int e = tid; e < kRows * 8 * DC; e += kThreads) {
-    const int r = e / (8 * DC), c = e % (8 * DC);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < a.Tq && c < nq4) x = load4(q + (r0 + r) * a.q.row_stride + 4 * c);
-    *reinterpret_cast<float4*>(qs + r * DP + 4 * c) = x;
-  }
-  float m[4], l[4], acc[4][4 * DC];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < 4 * DC; ++c) acc[i][c] = 0.f;
-  }
-  const long long shift = static_cast<long long>(a.Tk) - a.Tq;   // causal: key j for row i iff j <= i + shift
-  long long klast = a.Tk;
-  if (a.causal) klast = min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift);
-  // this CTA's share of the key tiles
-  const long long ktiles = klast > 0 ? (klast + kKeys - 1) / kKeys : 0;
-  const long long kend = min(klast, ktiles * (rank + 1) / S * kKeys);
-  for (long long k0 = ktiles * rank / S * kKeys; k0 < kend; k0 += kKeys) {
-    bool mine = false;
-    if (tid < kKeys) {
-      mine = k0 + tid < a.Tk && (!mask || mask[k0 + tid] != 0);
+  const long long shift = static_cast<long long>(a.Tk) - a.Tq;     // causal: key j for row i iff j <= i + shift
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+  const int dk = (a.D + 15) / 16;
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abortp = &ctl->abort_flag;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+    ok = __all_sync(0xffffffffu, okw) && ok;
+    return ok;
+  };
+  auto give_up = [&] {
+    if (lane == 0) {
+      ctl->abort_flag = 1;
+      atomicOr(a.err, kErrTimeout);
     }
-    // keys up to the last visible one, in eights
-    const uint32_t bits = __ballot_sync(0xffffffffu, mine);
-    if ((tid & 31) == 0 && tid < kKeys) words[tid >> 5] = bits;
-    if (tid < kKeys) ok[tid] = mine;
-    __syncthreads();
-    const uint32_t w0 = words[0], w1 = words[1];
-    if (!(w0 | w1)) {
-      __syncthreads();
-      continue;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->qready, kConvThreads / 32);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->kready[s], kConvThreads / 32);
+      mbar_init(&ctl->kempty[s], 1);
+      mbar_init(&ctl->vready[s], kConvThreads / 32);
+      mbar_init(&ctl->vempty[s], 1);
     }
-    const int groups = w1 ? 8 - (__clz(w1) >> 3) : 4 - (__clz(w0) >> 3);
-#pragma unroll 4
-    for (int e = tid; e < 8 * groups * 8 * DC; e += kThreads) {
-      const int r = e / (8 * DC), c = e % (8 * DC);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (ok[r] && c < nq4) {
-        x = load4(k + (k0 + r) * a.k.row_stride + 4 * c);
-        y = load4(v + (k0 + r) * a.v.row_stride + 4 * c);
+    for (int s = 0; s < kInfo; ++s) {
+      mbar_init(&ctl->ifull[s], 1);
+      mbar_init(&ctl->iempty[s], 1 + 4 + kConvThreads / 32);       // products, softmax, converters
+    }
+    mbar_init(&ctl->sfull[0], 1);
+    mbar_init(&ctl->sfull[1], 1);
+    mbar_init(&ctl->pready, 4);
+    mbar_init(&ctl->odone, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  // tile j's info, the slot given back; k0 < 0: no more tiles (or a wait ran out)
+  auto next = [&](uint32_t j) {
+    Info f;
+    f.k0 = -1;
+    const uint32_t is = j % kInfo;
+    if (wait(&ctl->ifull[is], (j / kInfo) & 1)) {
+      f = ctl->info[is];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->iempty[is]);
+    }
+    return f;
+  };
+
+  if (warp < 4) {
+    regs_give_up<kRegsIssue>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- tiles and key bits
+      long long klast = a.Tk;                       // keys that some row of this CTA may see
+      if (a.causal) klast = max(0ll, min(klast, min(static_cast<long long>(r0) + kRows, static_cast<long long>(a.Tq)) + shift));
+      long long full = a.Tk;                        // and those that every row sees (but for the mask)
+      if (a.causal) full = max(0ll, min(full, r0 + shift + 1));
+      const int all = static_cast<int>((klast + BN - 1) / BN), seen = static_cast<int>(full / BN);
+      const int lo = static_cast<int>(static_cast<long long>(all) * rank / S);
+      const int hi = static_cast<int>(static_cast<long long>(all) * (rank + 1) / S);
+      const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
+      uint8_t ahead[W];                             // mask bytes of the coming tile
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const long long key = static_cast<long long>(t) * BN + 32 * w + lane;
+          ahead[w] = t < hi && key < a.Tk ? (mask ? mask[key] : 1) : 0;
+        }
+      };
+      fetch(lo);
+      uint32_t n = 0;                               // tiles handed on
+      for (int t = lo; t <= hi && ok; ++t) {
+        const bool end = t == hi;
+        uint32_t bits[W], any = 0, every = 0xffffffffu;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          bits[w] = __ballot_sync(0xffffffffu, ahead[w] != 0);
+          any |= bits[w];
+          every &= bits[w];
+        }
+        if (!end) fetch(t + 1);
+        if (!end && !any) continue;
+        const uint32_t is = n % kInfo;
+        if (n >= kInfo && !wait(&ctl->iempty[is], ((n / kInfo) & 1) ^ 1)) break;
+        if (lane == 0) {
+          Info& f = ctl->info[is];
+          f.k0 = end ? -1 : t * BN;
+          f.plain = every == 0xffffffffu && t < seen;
+          f.words = bits[1] ? 2 : 1;
+          f.bits[0] = bits[0];
+          f.bits[1] = bits[1];
+          mbar_arrive(&ctl->ifull[is]);
+        }
+        __syncwarp();
+        ++n;
       }
-      *reinterpret_cast<float4*>(ks + r * DP + 4 * c) = x;
-      *reinterpret_cast<float4*>(vs + r * DP + 4 * c) = y;
+      if (!ok) give_up();
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- products
+      constexpr int kTerms[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};   // planes, small products first
+      const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);        // and N = the keys taken
+      const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
+      const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(kv));
+      const uint64_t vd = desc_mn_sw128(smem_u32(kv) + P::kKvBytes, BN * 128);
+      bool issued = false;
+      auto scores = [&](uint32_t j, int words) {
+        const uint32_t s = j % kStages;
+        if (!wait(&ctl->kready[s], (j / kStages) & 1)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int c = 0; c < DCH; ++c)
+            umma_ss_f16_x4_elect(tmem + 64 * (j & 1), qd + ((kTerms[i][0] * P::kQPlane + c * kRows * 128) >> 4),
+                                 kd + ((s * P::kStageBytes + kTerms[i][1] * P::kPlane + c * BN * 128) >> 4),
+                                 idesc_s | (static_cast<uint32_t>(words * 4) << 17), (i > 0 || c > 0) ? 1u : 0u);
+        issued = true;
+        umma_commit_elect(&ctl->sfull[j & 1]);
+        umma_commit_elect(&ctl->kempty[s]);
+      };
+      Info f = next(0);
+      if (f.k0 >= 0 && wait(&ctl->qready, 0)) scores(0, f.words);
+      for (uint32_t j = 0; f.k0 >= 0 && ok; ++j) {
+        const uint32_t s = j % kStages;
+        const Info g = next(j + 1);
+        if (ok && g.k0 >= 0) scores(j + 1, g.words);               // its buffer was read before P of tile j - 1 was ready
+        if (!ok || !wait(&ctl->vready[s], (j / kStages) & 1) || !wait(&ctl->pready, j & 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (w < f.words)
+              umma_ts_f16_x2_elect(tmem + kColO, tmem + kColP + 32 * kTerms[i][0] + 16 * w,
+                                   vd + ((s * P::kStageBytes + kTerms[i][1] * P::kPlane + w * 4096) >> 4), 2048 >> 4,
+                                   idesc_o, (i > 0 || w > 0) ? 1u : 0u);
+        umma_commit_elect(&ctl->odone);
+        umma_commit_elect(&ctl->vempty[s]);
+        f = g;
+      }
+      if (!ok) give_up();
+      if (issued) {                                                // what was issued ends before the CTA does
+        umma_commit_elect(&ctl->drain);
+        if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
+      }
+      __syncwarp();
     }
-    __syncthreads();
-    float s[4][8];
+  } else if (warp < 8) {
+    regs_take<kRegsSoft>();
+    // ---------------------------------------------------------------- softmax: one row per thread
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float m = -INFINITY, l = 0.f, acc[64 * DCH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int e = 0; e < 64 * DCH; ++e) acc[e] = 0.f;
+    // the last tile's output, once its product is done, and the rescaling of all so far
+    auto gather = [&](uint32_t j, float f) {
+      if (!wait(&ctl->odone, j & 1)) return;
+      tc_fence_after();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = 0.f;
-    auto dots = [&](auto half) {                                  // of the first 4 or all 8 groups of keys
-      constexpr int kGroups = decltype(half)::value ? 4 : 8;
-      for (int c = 0; c < nq4; ++c) {
-        float4 qv[4], kv[kGroups];
+      for (int c = 0; c < 4 * DCH; ++c) {
+        if (c >= dk) continue;
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
+        tmem_wait_ld_regs(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(qs + (rg + 16 * i) * DP + 4 * c);
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (cg + 8 * j) * DP + 4 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < kGroups; ++j)
-            s[i][j] = fmaf(qv[i].x, kv[j].x, fmaf(qv[i].y, kv[j].y, fmaf(qv[i].z, kv[j].z, fmaf(qv[i].w, kv[j].w, s[i][j]))));
+        for (int e = 0; e < 16; ++e) acc[16 * c + e] = (acc[16 * c + e] + __uint_as_float(o[e])) * f;
       }
     };
-    if (groups <= 4)
-      dots(std::true_type{});
-    else
-      dots(std::false_type{});
+    uint32_t j = 0;
+    for (;; ++j) {
+      const Info t = next(j);
+      if (t.k0 < 0) break;
+      uint32_t bits[W] = {t.bits[0], t.bits[1]};
+      if (a.causal && !t.plain) {                                  // keys up to the diagonal
+        const int v = static_cast<int>(max(0ll, min(r0 + r + shift - t.k0 + 1, static_cast<long long>(BN))));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long row = r0 + rg + 16 * i;
-      float top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool live = ok[cg + 8 * j] && (!a.causal || k0 + cg + 8 * j <= row + shift);
-        s[i][j] = live ? s[i][j] * qscale : -INFINITY;
-        top = fmaxf(top, s[i][j]);
-      }
-#pragma unroll
-      for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float mn = fmaxf(m[i], top);
-      const float base = mn == -INFINITY ? 0.f : mn;             // nothing seen yet: every weight is 0
-      const float f = ex2_approx(m[i] - base);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p = ex2_approx(s[i][j] - base);
-        sum += p;
-        ps[(rg + 16 * i) * kPitch + cg + 8 * j] = p;
-      }
-#pragma unroll
-      for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      l[i] = l[i] * f + sum;
-      m[i] = mn;
-#pragma unroll
-      for (int c = 0; c < 4 * DC; ++c) acc[i][c] *= f;
-    }
-    __syncwarp();                                                 // a row's weights come from its own warp
-#pragma unroll 2
-    for (int j4 = 0; j4 < 2 * groups; ++j4) {
-      float4 pv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(ps + (rg + 16 * i) * kPitch + 4 * j4);
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-#pragma unroll
-        for (int d = 0; d < DC; ++d) {
-          const float4 x = *reinterpret_cast<const float4*>(vs + (4 * j4 + jj) * DP + 32 * d + 4 * cg);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = jj == 0 ? pv[i].x : jj == 1 ? pv[i].y : jj == 2 ? pv[i].z : pv[i].w;
-            acc[i][4 * d] = fmaf(p, x.x, acc[i][4 * d]);
-            acc[i][4 * d + 1] = fmaf(p, x.y, acc[i][4 * d + 1]);
-            acc[i][4 * d + 2] = fmaf(p, x.z, acc[i][4 * d + 2]);
-            acc[i][4 * d + 3] = fmaf(p, x.w, acc[i][4 * d + 3]);
-          }
+        for (int w = 0; w < W; ++w) {
+          const int c = min(max(v - 32 * w, 0), 32);
+          bits[w] &= c == 32 ? 0xffffffffu : (1u << c) - 1u;
         }
       }
-    }
-    __syncthreads();
-  }
-  if (S == 1) {
+      if (!wait(&ctl->sfull[j & 1], (j >> 1) & 1)) break;
+      tc_fence_after();
+      float x[BN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long row = r0 + rg + 16 * i;
-      if (row >= a.Tq) continue;
-      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+      for (int w = 0; w < W; ++w) {
+        uint32_t(&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]);
+        if (w < t.words) tmem_ld_32x32b_x32(lane_base + 64 * (j & 1) + 32 * w, v);
+      }
 #pragma unroll
-      for (int d = 0; d < DC; ++d)
-        if (32 * d + 4 * cg < a.D)
-          store4(o + row * a.out.row_stride + 32 * d + 4 * cg,
-                 make_float4(acc[i][4 * d] * inv, acc[i][4 * d + 1] * inv, acc[i][4 * d + 2] * inv,
-                             acc[i][4 * d + 3] * inv));
-    }
-    return;
-  }
-  // The shares meet in shared memory, where the keys were: (O, m, l) of every row, in rank order.
-  float* ml = ps;                                                  // [64][2]
+      for (int w = 0; w < W; ++w) {
+        tmem_wait_ld_regs(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * w]));
+        if (!t.plain) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = rg + 16 * i;
+          for (int e = 0; e < 32; ++e) x[32 * w + e] = (bits[w] >> e) & 1u ? x[32 * w + e] : -INFINITY;
+        }
+      }
+      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int d = 0; d < DC; ++d)
-      *reinterpret_cast<float4*>(ks + r * DP + 32 * d + 4 * cg) =
-          make_float4(acc[i][4 * d], acc[i][4 * d + 1], acc[i][4 * d + 2], acc[i][4 * d + 3]);
-    if (cg == 0) {
-      ml[2 * r] = m[i];
-      ml[2 * r + 1] = l[i];
+      for (int e = 0; e < BN; e += 2) t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], x[e], x[e + 1]);
+      const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], m);   // NaN if any score was
+      const float base = top == -INFINITY ? 0.f : top * scale_log2;          // no key yet: every weight is 0
+      const float f = m == -INFINITY ? 0.f : ex2_approx((m - top) * scale_log2);
+      m = top;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < BN; ++e) {
+        x[e] = ex2_approx(fmaf(x[e], scale_log2, -base));
+        sum[e & 3] += x[e];
+      }
+      l = fmaf(l, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (j > 0) {
+        gather(j - 1, f);
+        if (!ok) break;
+      }
+      // P is free: the product that read it is done
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w >= t.words) continue;
+        uint32_t p0[16], p1[16], p2[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          uint32_t p[3];
+          planes(x[32 * w + 2 * e], x[32 * w + 2 * e + 1], p);
+          p0[e] = p[0];
+          p1[e] = p[1];
+          p2[e] = p[2];
+        }
+        tmem_st_32x32b_x16(lane_base + kColP + 16 * w, p0);
+        tmem_st_32x32b_x16(lane_base + kColP + 32 + 16 * w, p1);
+        tmem_st_32x32b_x16(lane_base + kColP + 64 + 16 * w, p2);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->pready);
     }
-  }
-  cluster_sync();
-  const uint32_t oo = smem_u32(ks), om = smem_u32(ml);
-  const int share = kRows / S;
-  for (int e = tid; e < share * nq4; e += kThreads) {
-    const int r = rank * share + e / nq4, c = e % nq4;
-    if (r0 + r >= a.Tq) continue;
-    float top = -INFINITY;
-    for (int s = 0; s < S; ++s) top = fmaxf(top, cluster_load1(cluster_map(om + 8 * r, s)));
-    float total = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < S; ++s) {
-      const float ms = cluster_load1(cluster_map(om + 8 * r, s));
-      if (ms == -INFINITY) continue;                               // a share without a key for this row
-      const float f = ex2_approx(ms - top);
-      const float4 v = cluster_load4(cluster_map(oo + 4 * (r * DP + 4 * c), s));
-      total = fmaf(f, cluster_load1(cluster_map(om + 8 * r + 4, s)), total);
-      y.x = fmaf(f, v.x, y.x);
-      y.y = fmaf(f, v.y, y.y);
-      y.z = fmaf(f, v.z, y.z);
-      y.w = fmaf(f, v.w, y.w);
+    if (ok && j > 0) gather(j - 1, 1.f);
+    if (!ok) give_up();
+    if (S == 1) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float* o = static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride;
+      if (ok && r0 + r < a.Tq) {
+#pragma unroll
+        for (int c = 0; c < 16 * DCH; ++c)
+          if (4 * c < a.D)
+            store4(o + 4 * c, make_float4(acc[4 * c] * inv, acc[4 * c + 1] * inv, acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
+      }
+    } else {
+      // this CTA's share, over Q's planes (their last reader is done): row r's 16-byte pieces c at c ^ (r & 15)
+      ctl->m[r] = m;
+      ctl->l[r] = l;
+#pragma unroll
+      for (int c = 0; c < 16 * DCH; ++c)
+        *reinterpret_cast<float4*>(qs + r * (256 * DCH) + ((c ^ (r & 15)) << 4)) =
+            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    store4(o + (r0 + r) * a.out.row_stride + 4 * c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+  } else {
+    regs_give_up<kRegsConv>();
+    // ---------------------------------------------------------------- converters
+    constexpr int kRow4 = 16 * DCH;                 // 16-byte pieces of a row, 64 columns each chunk
+    const int t = threadIdx.x - 256;
+    const int c4 = t % kRow4, nq4 = a.D / 4;
+    // piece (row, c4) of a plane: four bf16 of a 128-byte swizzled row
+    auto put = [&](uint8_t* tile0, int plane_bytes, int chunk_bytes, int row, const float4& v) {
+      uint32_t lo[3], hi[3];
+      planes(v.x, v.y, lo);
+      planes(v.z, v.w, hi);
+      const int c = c4 & 15;
+      uint8_t* at = tile0 + (c4 >> 4) * chunk_bytes + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(at + i * plane_bytes) = make_uint2(lo[i], hi[i]);
+    };
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kStep = kConvThreads / kRow4;     // rows between a thread's pieces
+    const float* q = static_cast<const float*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
+    const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
+    const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
+    float4 kr[BN / kStep], vr[BN / kStep];
+    auto fetch = [&](const Info& f) {
+#pragma unroll
+      for (int i = 0; i < BN / kStep; ++i) {
+        const int row = t / kRow4 + i * kStep;
+        const bool live = f.k0 >= 0 && c4 < nq4 && ((f.bits[row >> 5] >> (row & 31)) & 1u);
+        kr[i] = live ? load4(k + (f.k0 + static_cast<long long>(row)) * a.k.row_stride + 4 * c4) : zero;
+        vr[i] = live ? load4(v + (f.k0 + static_cast<long long>(row)) * a.v.row_stride + 4 * c4) : zero;
+      }
+    };
+    Info f = next(0);
+    fetch(f);
+    if (f.k0 >= 0) {
+#pragma unroll 4
+      for (int row = t / kRow4; row < kRows; row += kStep)
+        put(qs, P::kQPlane, kRows * 128, row,
+            r0 + row < a.Tq && c4 < nq4 ? load4(q + (r0 + static_cast<long long>(row)) * a.q.row_stride + 4 * c4) : zero);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->qready);
+    }
+    for (uint32_t j = 0; f.k0 >= 0 && ok; ++j) {
+      const uint32_t s = j % kStages, ph = (j / kStages) & 1;
+      uint8_t* ks = kv + s * P::kStageBytes;
+      if (j >= kStages && !wait(&ctl->kempty[s], ph ^ 1)) break;
+#pragma unroll
+      for (int i = 0; i < BN / kStep; ++i) put(ks, P::kPlane, BN * 128, t / kRow4 + i * kStep, kr[i]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->kready[s]);
+      if (j >= kStages && !wait(&ctl->vempty[s], ph ^ 1)) break;
+#pragma unroll
+      for (int i = 0; i < BN / kStep; ++i) put(ks + P::kKvBytes, P::kPlane, BN * 128, t / kRow4 + i * kStep, vr[i]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->vready[s]);
+      f = next(j + 1);
+      fetch(f);
+    }
+    if (!ok) give_up();
   }
-  __syncwarp();
-  cluster_sync();                                                  // nobody leaves while its shared memory is read
+  tc_fence_before();
+  __syncthreads();
+  // tensor memory is given back before any wait for another CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (S > 1) {
+    cluster_sync();
+    const uint32_t om = smem_u32(ctl->m), ol = smem_u32(ctl->l), oo = smem_u32(qs);
+    const int pieces = a.D / 4, share = kRows / S;
+    for (int i = threadIdx.x; i < share * pieces; i += kThreads) {
+      const int r = rank * share + i / pieces, c = i % pieces;
+      if (r0 + r >= a.Tq) continue;
+      float top = -INFINITY;
+      for (int s = 0; s < S; ++s) top = fmaxf(top, cluster_load1(cluster_map(om + 4 * r, s)));
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < S; ++s) {
+        const float ms = cluster_load1(cluster_map(om + 4 * r, s));
+        if (ms == -INFINITY) continue;              // a share without a key for this row
+        const float f = ex2_approx((ms - top) * scale_log2);
+        const float4 v = cluster_load4(cluster_map(oo + r * (256 * DCH) + ((c ^ (r & 15)) << 4), s));
+        l = fmaf(f, cluster_load1(cluster_map(ol + 4 * r, s)), l);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride + 4 * c,
+             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    __syncwarp();
+    cluster_sync();                                 // nobody leaves while its shared memory is read
+  }
 }
 
-template <int DC>
+template <int DCH>
 cudaError_t go(const AttentionArgs& a, unsigned work, int S, cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(float) * ((kRows + 2 * kKeys) * (32 * DC + 4) + kRows * kPitch);
-  cudaError_t e = allow_smem<attention_f32_kernel<DC>>(bytes);
+  static_assert(Plan<DCH>::kSmem <= 227 * 1024, "shared memory");
+  cudaError_t e = allow_smem<attention_f32_kernel<DCH>>(Plan<DCH>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_cluster(attention_f32_kernel<DC>, dim3(work * S), kThreads, bytes, S, stream, a, S);
+  return launch_cluster(attention_f32_kernel<DCH>, dim3(work * S), kThreads, Plan<DCH>::kSmem, S, stream, a, S);
 }
 
-}  // namespace att
+}  // namespace att32
 
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
-  const long long ntiles = (static_cast<long long>(a.Tq) + att::kRows - 1) / att::kRows;
-  const unsigned work = static_cast<unsigned>(ntiles * a.q.heads * a.B);
-  // few query tiles: a cluster shares the keys of one, while that keeps to two CTAs per SM
-  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + att::kKeys - 1) / att::kKeys);
+  using namespace att32;
+  const long long work = (static_cast<long long>(a.Tq) + kRows - 1) / kRows * a.q.heads * a.B;
+  // few query tiles: a cluster shares the keys of one, while that keeps to one CTA per SM
+  const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + BN - 1) / BN);
   int S = 1;
-  while (S < 8 && static_cast<long long>(work) * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
-  switch ((a.D + 31) / 32) {
-    case 1:
-      return att::go<1>(a, work, S, stream);
-    case 2:
-      return att::go<2>(a, work, S, stream);
-    case 3:
-      return att::go<3>(a, work, S, stream);
-    default:
-      return att::go<4>(a, work, S, stream);
-  }
+  while (S < 8 && work * S * 2 <= num_sms && ktiles >= 2 * S) S *= 2;
+  const unsigned w = static_cast<unsigned>(work);
+  return a.D <= 64 ? go<1>(a, w, S, stream) : go<2>(a, w, S, stream);
 }
 
 }  // namespace gkd

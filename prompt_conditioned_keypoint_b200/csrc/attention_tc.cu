@@ -520,15 +520,6 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
   }
 }
 
-// Attention over no keys: zeros.
-__global__ void __launch_bounds__(128) zero_kernel(__nv_bfloat16* out, long long bs, long long rs, long long hs, int B,
-                                                   int T, int heads, int D) {
-  for (long long row = blockIdx.x; row < static_cast<long long>(B) * T; row += gridDim.x)
-    for (int i = threadIdx.x; i < heads * (D / 8); i += blockDim.x)
-      *reinterpret_cast<uint4*>(out + row / T * bs + row % T * rs + i / (D / 8) * hs + i % (D / 8) * 8) =
-          make_uint4(0u, 0u, 0u, 0u);
-}
-
 bool encode(CUtensorMap* m, const HeadsView& t, int B, int rows, int D, int box_rows) {
   EncodeTiledFn enc = get_encode_tiled();
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(t.heads),
@@ -550,17 +541,27 @@ cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
   return launch_cluster(attention_kernel<DCH, MASK>, dim3(work * S), kThreads, bytes, S, stream, a, S);
 }
 
+// Attention over no keys: zeros. `row16`: 16-byte pieces of a head's row; strides in bytes.
+__global__ void __launch_bounds__(128) zero_kernel(uint8_t* out, long long bs, long long rs, long long hs, int B, int T,
+                                                   int heads, int row16) {
+  for (long long row = blockIdx.x; row < static_cast<long long>(B) * T; row += gridDim.x)
+    for (int i = threadIdx.x; i < heads * row16; i += blockDim.x)
+      *reinterpret_cast<uint4*>(out + row / T * bs + row % T * rs + i / row16 * hs + i % row16 * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+}
+
 }  // namespace atc
+
+cudaError_t launch_attention_none(const AttentionArgs& a, int size, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(a.B) * a.Tq;
+  atc::zero_kernel<<<static_cast<unsigned>(rows < 65536 ? rows : 65536), 128, 0, stream>>>(
+      static_cast<uint8_t*>(a.out.data), a.out.batch_stride * size, a.out.row_stride * size, a.out.head_stride * size, a.B,
+      a.Tq, a.q.heads, a.D * size / 16);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t stream, const char** why) {
   using namespace atc;
-  if (a.Tk == 0) {
-    const long long rows = static_cast<long long>(a.B) * a.Tq;
-    zero_kernel<<<static_cast<unsigned>(rows < 65536 ? rows : 65536), 128, 0, stream>>>(
-        static_cast<__nv_bfloat16*>(a.out.data), a.out.batch_stride, a.out.row_stride, a.out.head_stride, a.B, a.Tq,
-        a.q.heads, a.D);
-    return cudaGetLastError();
-  }
   Args p{};
   if (!encode(&p.q, a.q, a.B, a.Tq, a.D, kRows) || !encode(&p.k, a.k, a.B, a.Tk, a.D, BN) ||
       !encode(&p.v, a.v, a.B, a.Tk, a.D, BN)) {

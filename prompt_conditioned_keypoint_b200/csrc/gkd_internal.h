@@ -197,6 +197,7 @@ struct AttentionArgs {
   unsigned* err;
   unsigned long long wait_limit_ns;
 };
+cudaError_t launch_attention_none(const AttentionArgs& a, int size, cudaStream_t stream);   // Tk = 0: zeros
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16
 
