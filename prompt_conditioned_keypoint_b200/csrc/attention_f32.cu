@@ -43,12 +43,12 @@ struct Info {                                       // one key tile
 
 template <int DCH>
 struct Plan {
-  static constexpr int kStages = DCH == 1 ? 2 : 1;
+  static constexpr int kStages = DCH == 1 ? 2 : 1, kOBufs = DCH == 1 ? 2 : 1;
   static constexpr int kQPlane = kRows * 128 * DCH, kPlane = BN * 128 * DCH;        // bytes
   static constexpr int kKvBytes = 3 * kPlane, kStageBytes = 2 * kKvBytes;           // K's planes, then V's
   struct Ctl {
     uint64_t qready, kready[kStages], kempty[kStages], vready[kStages], vempty[kStages];
-    uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready, odone, drain;
+    uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], odone[2], drain;
     Info info[kInfo];
     uint32_t tmem_base;
     int abort_flag;
@@ -57,7 +57,10 @@ struct Plan {
   static constexpr size_t kSmem = 1024 + 3 * kQPlane + kStages * kStageBytes + sizeof(Ctl);
 };
 
-constexpr uint32_t kColP = 128, kColO = 256;        // scores at 0 and 64, P's planes of 32 columns, the tile's output
+// Tensor memory: scores at 0 and 64, P's three planes of 32 columns twice, the tile's output (twice for heads
+// up to 64: the next tile's product then need not wait until it is added up). Buffers and barriers go by the
+// parity of the tile: a softmax warp may be a tile ahead of another.
+constexpr uint32_t kColP = 128, kColO = 320;
 
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t lbo) {
   return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) | (64ull << 32) |
@@ -118,10 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       mbar_init(&ctl->ifull[s], 1);
       mbar_init(&ctl->iempty[s], 1 + 4 + kConvThreads / 32);       // products, softmax, converters
     }
-    mbar_init(&ctl->sfull[0], 1);
-    mbar_init(&ctl->sfull[1], 1);
-    mbar_init(&ctl->pready, 4);
-    mbar_init(&ctl->odone, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->sfull[s], 1);
+      mbar_init(&ctl->pready[s], 4);
+      mbar_init(&ctl->odone[s], 1);
+    }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -223,17 +227,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         const uint32_t s = j % kStages;
         const Info g = next(j + 1);
         if (ok && g.k0 >= 0) scores(j + 1, g.words);               // its buffer was read before P of tile j - 1 was ready
-        if (!ok || !wait(&ctl->vready[s], (j / kStages) & 1) || !wait(&ctl->pready, j & 1)) break;
+        if (!ok || !wait(&ctl->vready[s], (j / kStages) & 1) || !wait(&ctl->pready[j & 1], (j >> 1) & 1)) break;
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 6; ++i)
 #pragma unroll
           for (int w = 0; w < W; ++w)
             if (w < f.words)
-              umma_ts_f16_x2_elect(tmem + kColO, tmem + kColP + 32 * kTerms[i][0] + 16 * w,
+              umma_ts_f16_x2_elect(tmem + kColO + 64 * (j % P::kOBufs), tmem + kColP + 96 * (j & 1) + 32 * kTerms[i][0] + 16 * w,
                                    vd + ((s * P::kStageBytes + kTerms[i][1] * P::kPlane + w * 4096) >> 4), 2048 >> 4,
                                    idesc_o, (i > 0 || w > 0) ? 1u : 0u);
-        umma_commit_elect(&ctl->odone);
+        umma_commit_elect(&ctl->odone[j & 1]);
         umma_commit_elect(&ctl->vempty[s]);
         f = g;
       }
@@ -254,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     for (int e = 0; e < 64 * DCH; ++e) acc[e] = 0.f;
     // the last tile's output, once its product is done, and the rescaling of all so far
     auto gather = [&](uint32_t j, float f) {
-      if (!wait(&ctl->odone, j & 1)) return;
+      if (!wait(&ctl->odone[j & 1], (j >> 1) & 1)) return;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 4 * DCH; ++c) {
         if (c >= dk) continue;
         uint32_t o[16];
-        tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
+        tmem_ld_32x32b_x16(lane_base + kColO + 64 * (j % P::kOBufs) + 16 * c, o);
         tmem_wait_ld_regs(o);
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[16 * c + e] = (acc[16 * c + e] + __uint_as_float(o[e])) * f;
@@ -309,11 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         sum[e & 3] += x[e];
       }
       l = fmaf(l, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-      if (j > 0) {
-        gather(j - 1, f);
-        if (!ok) break;
-      }
-      // P is free: the product that read it is done
+      // this buffer of P is free: the product that read it last, of tile j - 2, has been gathered
+      const uint32_t pcol = lane_base + kColP + 96 * (j & 1);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         if (w >= t.words) continue;
@@ -326,14 +327,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
           p1[e] = p[1];
           p2[e] = p[2];
         }
-        tmem_st_32x32b_x16(lane_base + kColP + 16 * w, p0);
-        tmem_st_32x32b_x16(lane_base + kColP + 32 + 16 * w, p1);
-        tmem_st_32x32b_x16(lane_base + kColP + 64 + 16 * w, p2);
+        tmem_st_32x32b_x16(pcol + 16 * w, p0);
+        tmem_st_32x32b_x16(pcol + 32 + 16 * w, p1);
+        tmem_st_32x32b_x16(pcol + 64 + 16 * w, p2);
       }
       tmem_wait_st();
+      if (P::kOBufs == 1 && j > 0) {                // the product overwrites the last tile's output
+        gather(j - 1, f);
+        if (!ok) break;
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->pready);
+      if (lane == 0) mbar_arrive(&ctl->pready[j & 1]);
+      if (P::kOBufs == 2 && j > 0) {                // under this tile's product
+        gather(j - 1, f);
+        if (!ok) break;
+      }
     }
     if (ok && j > 0) gather(j - 1, 1.f);
     if (!ok) give_up();
@@ -386,17 +395,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         vr[i] = live ? load4(v + (f.k0 + static_cast<long long>(row)) * a.v.row_stride + 4 * c4) : zero;
       }
     };
+    // Q first, half of it at a time: its loads wait for no mask
+    auto fetch_q = [&](float4* to, int half) {
+#pragma unroll
+      for (int i = 0; i < BN / kStep; ++i) {
+        const int row = 64 * half + t / kRow4 + i * kStep;
+        to[i] = r0 + row < a.Tq && c4 < nq4 ? load4(q + (r0 + static_cast<long long>(row)) * a.q.row_stride + 4 * c4) : zero;
+      }
+    };
+    auto put_q = [&](const float4* from, int half) {
+#pragma unroll
+      for (int i = 0; i < BN / kStep; ++i) put(qs, P::kQPlane, kRows * 128, 64 * half + t / kRow4 + i * kStep, from[i]);
+    };
+    fetch_q(kr, 0);
+    fetch_q(vr, 1);
+    put_q(kr, 0);
+    put_q(vr, 1);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->qready);
     Info f = next(0);
     fetch(f);
-    if (f.k0 >= 0) {
-#pragma unroll 4
-      for (int row = t / kRow4; row < kRows; row += kStep)
-        put(qs, P::kQPlane, kRows * 128, row,
-            r0 + row < a.Tq && c4 < nq4 ? load4(q + (r0 + static_cast<long long>(row)) * a.q.row_stride + 4 * c4) : zero);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->qready);
-    }
     for (uint32_t j = 0; f.k0 >= 0 && ok; ++j) {
       const uint32_t s = j % kStages, ph = (j / kStages) & 1;
       uint8_t* ks = kv + s * P::kStageBytes;
