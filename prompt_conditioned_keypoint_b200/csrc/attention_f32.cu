@@ -450,14 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     for (int i = threadIdx.x; i < share * pieces; i += kThreads) {
       const int r = rank * share + i / pieces, c = i % pieces;
       if (r0 + r >= a.Tq) continue;
-      float top = -INFINITY;
+      float top = -INFINITY;                        // loops without branches: the loads are in flight together
+#pragma unroll 8
       for (int s = 0; s < S; ++s) top = fmaxf(top, cluster_load1(cluster_map(om + 4 * r, s)));
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float ms = cluster_load1(cluster_map(om + 4 * r, s));
-        if (ms == -INFINITY) continue;              // a share without a key for this row
-        const float f = ex2_approx((ms - top) * scale_log2);
+        const float f = ms == -INFINITY ? 0.f : ex2_approx((ms - top) * scale_log2);   // 0: a share without a key for this row
         const float4 v = cluster_load4(cluster_map(oo + r * (256 * DCH) + ((c ^ (r & 15)) << 4), s));
         l = fmaf(f, cluster_load1(cluster_map(ol + 4 * r, s)), l);
         o.x = fmaf(f, v.x, o.x);

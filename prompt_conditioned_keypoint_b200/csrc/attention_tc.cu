@@ -36,6 +36,7 @@ namespace atc {
 
 constexpr int kSoftWarps = 4, kThreads = 32 * (2 + kSoftWarps), kRows = 128, kKvStages = 2, kInfo = 4;
 constexpr int BN = 64, W = BN / 32;                 // keys per tile, words of key bits
+constexpr int kMaxSplit = 16;                       // CTAs of a cluster (above 8 the kernel asks for it)
 constexpr float kGrow = 8.f;                        // rescale O when a maximum grew by more than this (log2)
 
 struct Args {
@@ -496,14 +497,15 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     for (int i = threadIdx.x; i < share * pieces; i += kThreads) {
       const int r = rank * share + i / pieces, c = i % pieces;
       if (r0 + r >= a.Tq) continue;
-      float m = -INFINITY;
+      float m = -INFINITY;                          // loops without branches: the loads are in flight together
+#pragma unroll 8
       for (int s = 0; s < S; ++s) m = fmaxf(m, cluster_load1(cluster_map(om + 4 * r, s)));
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float ms = cluster_load1(cluster_map(om + 4 * r, s));
-        if (ms == -INFINITY) continue;              // a share without a key for this row
-        const float f = ex2_approx((ms - m) * a.scale_log2);
+        const float f = ms == -INFINITY ? 0.f : ex2_approx((ms - m) * a.scale_log2);   // 0: a share without a key for this row
         const float4 v = cluster_load4(cluster_map(oo + r * (256 * DCH) + ((c ^ (r & 15)) << 4), s));
         l = fmaf(f, cluster_load1(cluster_map(ol + 4 * r, s)), l);
         o.x = fmaf(f, v.x, o.x);
@@ -536,7 +538,7 @@ template <int DCH, bool MASK>
 cudaError_t go(const Args& a, int S, unsigned work, cudaStream_t stream) {
   constexpr size_t bytes = 1024 + kRows * 128 * DCH + 2 * kKvStages * BN * 128 * DCH + sizeof(Ctl);
   static_assert((DCH == 1 ? 4 : 2) * (bytes + 1024) <= 228 * 1024, "CTAs per SM");
-  cudaError_t e = allow_smem<attention_kernel<DCH, MASK>>(bytes);
+  cudaError_t e = allow_smem<attention_kernel<DCH, MASK>>(bytes, true);
   if (e != cudaSuccess) return e;
   return launch_cluster(attention_kernel<DCH, MASK>, dim3(work * S), kThreads, bytes, S, stream, a, S);
 }
@@ -588,7 +590,7 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_
   const long long work = static_cast<long long>(p.ntiles) * a.q.heads * a.B;
   const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + BN - 1) / BN);
   int S = 1;
-  while (S < 8 && work * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
+  while (S < kMaxSplit && work * S * 2 <= 2 * num_sms && ktiles >= 2 * S) S *= 2;
   const unsigned w = static_cast<unsigned>(work);
   if (a.mask) return a.D <= 64 ? go<1, true>(p, S, w, stream) : go<2, true>(p, S, w, stream);
   return a.D <= 64 ? go<1, false>(p, S, w, stream) : go<2, false>(p, S, w, stream);

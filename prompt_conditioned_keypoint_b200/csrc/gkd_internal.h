@@ -109,9 +109,9 @@ cudaError_t launch_pool_tc(const float* support, int B, int h, int w, int C, con
 // ---------------------------------------------------------------------------
 // Operators of the transformer blocks (gkd_blocks.h)
 // ---------------------------------------------------------------------------
-// Allows a kernel its dynamic shared memory, once per kernel and device.
+// Allows a kernel its dynamic shared memory (and clusters of 16 CTAs), once per kernel and device.
 template <auto* Kernel>
-cudaError_t allow_smem(size_t bytes) {
+cudaError_t allow_smem(size_t bytes, bool cluster16 = false) {
   static std::atomic<unsigned long long> done{0};    // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -119,6 +119,7 @@ cudaError_t allow_smem(size_t bytes) {
   const unsigned long long bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && cluster16) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
       if (a.residual) res = load4(a.residual + t * a.residual_stride + c);
       const uint32_t at = r * 512 + ((lane ^ (r & 31)) << 4);
       float z[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float4 v = S > 1 ? cluster_load4(cluster_map(base + at, s)) : *reinterpret_cast<const float4*>(smem + at);
         z[0] += v.x;

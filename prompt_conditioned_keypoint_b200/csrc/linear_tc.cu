@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
       if (a.residual) res = load4(static_cast<const TO*>(a.residual) + t * a.residual_stride + c);
       float4 y = b;
       const uint32_t at = base + (n * 128 + 4 * lane) * 4;
+#pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float4 v = S > 1 ? cluster_load4(cluster_map(at, s)) : *reinterpret_cast<const float4*>(part + n * 128 + 4 * lane);
         y.x += v.x;
