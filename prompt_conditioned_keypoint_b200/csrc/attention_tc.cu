@@ -28,6 +28,15 @@
 // joins (O, m, l) through shared memory in rank order.
 // The weights are rounded to bf16 for the second product (the operand type); their
 // sum l is taken from the fp32 values.
+//
+// Measured (B200, in a graph): 8 x 2309 rows of 20 heads of 64 344 us = 635 TFLOP/s; 12
+// heads of 128 274 us = 955; 64 x 80 rows over 576 keys 41 us; one row over 2304 keys
+// 12.2 us. Bound by the chain's instructions and latencies: on 2 x 2309 rows the
+// exponentials keep the special-function unit 45% busy, the tensor pipe is at 22%, 45% of
+// the issue slots are taken. Tried and slower for heads of 64: tiles of 128 keys at two
+// CTAs per SM (394 to 420 us in six forms: one or two threads per row, weights beside the
+// scores, a share of the exponentials on the fma units, 200 registers by giving up the
+// others'); scores held in registers at three CTAs per SM (406 us).
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
@@ -348,31 +357,42 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       if (!wait(&ctl->sfull[j % kBufs], (j / kBufs) & 1)) break;
       tc_fence_after();
       const uint32_t scores = lane_base + 64 * (j % kBufs);
+      // Hidden keys: -inf over their scores first, so that what follows is the same code
+      // without tests for every tile. (With the tests inside it 8 x 2309 rows took 386 us
+      // against 344; a second copy of it for whole tiles took 335, but 80 x 77 causal rows
+      // under a mask 35.8 against 30.9.)
+      if (!plain) {
+#pragma unroll 1
+        for (int g = 0; g < 2 * W; ++g) {
+          uint32_t x[16] = {};
+          if (g < 2 * words) {
+            tmem_ld_32x32b_x16(scores + 16 * g, x);
+            tmem_wait_ld_regs(x);
+          }
+          const uint32_t b16 = (g < 2 ? bits[0] : bits[1]) >> (16 * (g & 1));
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;
+          tmem_st_32x32b_x16(scores + 16 * g, x);
+        }
+        tmem_wait_st();
+      }
       // Groups of 16 scores. With two CTAs per SM a tile's scores stay in registers; with
       // four they are read twice, for the maximum and for the weights, and a group is on
       // its way while the one before is worked on.
       uint32_t v[kHold ? 2 * W : 2][16];
-      auto hide = [&](uint32_t(&x)[16], int g) {
-        const uint32_t b16 = bits[g >> 1] >> (16 * (g & 1));
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;   // -inf
-      };
       float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       auto load = [&](int g) { tmem_ld_32x32b_x16(scores + 16 * g, v[kHold ? g : g & 1]); };
       load(0);
       if (kHold) {
 #pragma unroll
-        for (int g = 1; g < 2 * W; ++g)
-          if (g < 2 * words) load(g);
+        for (int g = 1; g < 2 * W; ++g) load(g);
       }
 #pragma unroll
       for (int g = 0; g < 2 * W; ++g) {
-        if (g >= 2 * words) continue;
         uint32_t(&x)[16] = v[kHold ? g : g & 1];
         tmem_wait_ld_regs(x);
-        if (!kHold && g + 1 < 2 * W && g + 1 < 2 * words) load(g + 1);
-        if (!plain) hide(x, g);
+        if (!kHold && g + 1 < 2 * W) load(g + 1);
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
           t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
@@ -390,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
           // formed, and with one buffer the last one did too
           if (kBufs == 2 && !wait(&ctl->pvdone, (j - 1) & 1)) break;
           tc_fence_after();
+#pragma unroll 1
           for (int c = 0; c < ochunks; ++c) {
             uint32_t o[16];
             tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
@@ -406,12 +427,10 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       if (!kHold) load(0);
 #pragma unroll
       for (int g = 0; g < 2 * W; ++g) {
-        if (g >= 2 * words) continue;
         uint32_t(&x)[16] = v[kHold ? g : g & 1];
         if (!kHold) {
           tmem_wait_ld_regs(x);
-          if (g + 1 < 2 * W && g + 1 < 2 * words) load(g + 1);
-          if (!plain) hide(x, g);
+          if (g + 1 < 2 * W) load(g + 1);
         }
         uint32_t p[8];
 #pragma unroll

@@ -8,8 +8,13 @@
 // The tensor core truncates each step's sum, so a long sum drifts towards zero (at 1024
 // channels by 2.4e-6 of the result for plain TF32): the large products and the small
 // ones have accumulators of their own, and the epilogue warps add both up in fp32
-// after every 64 channels. Measured error at 1024 channels: 00 (fp32 fused
-// multiply-adds: 2.5e-7).
+// after every 64 channels. Measured error at 1024 and 4096 channels: 2.9e-7 and 3.1e-7 of
+// the result (fp32 products by the library: 5.7e-7 and 1.1e-6).
+//
+// Measured (B200, in a graph): 1360 x 1024 -> 1024 35 us (64 x 64 tiles on the fp32 units
+// took 120), 80 rows 10.2 us. Bound by shared memory: a stage moves 160 KB through it (32
+// read and 32 written by the converters, 96 read by the products) where the products
+// alone would take 768 clocks.
 //
 // A CTA has a 128 x 128 tile of the output, 18 warps:
 //   warp 0       TMA: stages of 32 channels of x and of weight (128B-swizzled);
