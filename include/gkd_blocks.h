@@ -70,8 +70,10 @@ typedef struct gkd_heads {
  *             It may be `out` itself (with the same stride).
  *   out       [T][Cout], rows out_stride apart, out_dt = GKD_BF16 or GKD_F32
  *             (dt = GKD_F32 takes GKD_F32 only). Columns past Cout are left alone.
- * Products and sums in fp32 or better, the epilogue in fp32, one rounding to
- * out_dt. `out` must not overlap x or weight.
+ * dt = GKD_BF16: exact products, sums in fp32. dt = GKD_F32: every operand as a pair
+ * of TF32 numbers, three products per term, each term within 2^-20 of its fp32
+ * product; x and weight must be finite (an infinity gives NaN). The epilogue is in
+ * fp32, with one rounding to out_dt. `out` must not overlap x or weight.
  * Limits: 0 <= T < 2^31, 8 <= Cin, Cout <= 65536, both multiples of 8, strides
  * at least the row's length.
  */
@@ -130,7 +132,9 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  *   out      as q. It must not overlap the inputs.
  * dt = GKD_BF16: tensor-core products with fp32 accumulation; maxima, sums and
  * exponentials in fp32; the weights p_j are rounded to bf16 for the product with v
- * (their sum is not). dt = GKD_F32: all in fp32.
+ * (their sum is not). dt = GKD_F32: every operand as three bf16 numbers (24 bits), six
+ * products per term, the rest in fp32; visible values must be finite and below 2^127 in
+ * magnitude (others give NaN). A row with a NaN or infinite score is NaN.
  * Limits: 0 <= B <= 65535, 0 <= Tq, Tk < 2^31 - 256, 8 <= D <= 128, D % 8 == 0,
  * 1 <= heads <= 1024, scale finite and positive.
  */

@@ -9,8 +9,14 @@
 // number, then sine and cosine in fp32. A thread holds both halves of V pairs, so
 // the rotation needs no exchange between threads; a head has D / (2 V) lanes, next to
 // one another in a warp, and the norm's sum goes over them by shuffles. Which
-// elements a thread takes is the same for all of its heads. Its loads (kItems heads of
-// two vectors each) are all issued before the angles are formed and are in flight meanwhile.
+// elements a thread takes is the same for all of its heads. Its loads (kItems heads
+// of two vectors each) are all issued before the angles are formed and are in flight
+// meanwhile.
+//
+// Measured (B200, in a graph): 64 x 581 rows of 2 x 20 heads of 64 63 us = 6.0 TB/s (92% of
+// the copy rate), 80 us with norms; 2 x 4608 rows of 20 fp32 heads of 80 with norms 29 us
+// = 4.1 TB/s. CTAs of 256 threads took 68, 87 and 32 us; a warp per row with its angles
+// and weights in registers 73, 104 and 35.
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
