@@ -91,6 +91,26 @@ LINEAR = [
     (3000, 200, 1000, "f32", "f32", "quick_gelu", True, True, True),
 ]
 
+# every tile width of the kernel for many rows (256, 192 and 128 columns), several tiles per CTA, both output types,
+# with and without a residual
+LINEAR += [
+    (4700, 264, 1024, "bf16", "bf16", "gelu", True, False, False),
+    (9400, 72, 1000, "bf16", "bf16", "none", True, False, True),
+    (4700, 1096, 1024, "bf16", "f32", "none", True, True, True),
+    (9400, 520, 1024, "bf16", "f32", "relu", False, False, False),
+    (5000, 200, 1032, "bf16", "bf16", "gelu", True, False, False),
+    (5000, 1096, 1032, "bf16", "f32", "none", True, False, False),
+    (1360, 520, 808, "bf16", "bf16", "quick_gelu", True, False, False),
+    (1360, 1096, 808, "bf16", "f32", "none", True, True, True),
+    (1400, 1096, 800, "bf16", "f32", "gelu", True, False, False),
+    (20000, 64, 8, "bf16", "bf16", "none", True, True, True),
+    (3, 8192, 24, "bf16", "f32", "none", True, False, False),
+    (700, 9000, 72, "bf16", "f32", "none", True, False, True),
+    (5, 65536, 16, "bf16", "bf16", "none", True, False, False),
+    (5, 8, 65536, "bf16", "bf16", "none", True, False, False),
+    (130, 4104, 136, "f32", "f32", "none", True, False, True),
+]
+
 
 def linear_case(T, Cin, Cout, dt, odt, act, bias, scale, res, seed=1):
     x, w = rand(seed, T, Cin, dt=dt), rand(seed + 1, Cout, Cin, dt=dt, std=Cin ** -0.5)
@@ -329,6 +349,19 @@ ATTENTION = [
     (1, 581, 581, 2, 2, 96, "f32", 0, "all"),
 ]
 
+# many key tiles per CTA, so that every ring turns over, whole and partial tiles mixed
+ATTENTION += [
+    (4, 300, 3001, 6, 2, 64, "bf16", 0, "holes"),
+    (4, 300, 3001, 6, 6, 128, "bf16", 0, "holes"),
+    (8, 700, 900, 8, 8, 80, "bf16", 1, "holes"),
+    (8, 700, 900, 8, 4, 64, "bf16", 1, "all"),
+    (2, 129, 2049, 16, 4, 128, "bf16", 0, "prefix"),
+    (4, 300, 1500, 6, 2, 64, "f32", 0, "holes"),
+    (4, 300, 1500, 6, 6, 128, "f32", 0, "holes"),
+    (8, 400, 500, 8, 4, 72, "f32", 1, "holes"),
+    (1, 5, 3001, 4, 4, 128, "f32", 0, "prefix"),
+]
+
 
 def attention_case(case, seed=21):
     B, Tq, Tk, H, Hk, D, dt, causal, kind = case
@@ -403,6 +436,25 @@ def test_attention_keys_past_32_bit_offsets(dt):
     gk.gkd_attention(q, k, v, DT[dt][1], 1, 3, Tk, D, 0.5, 0, None, 0, out)
     settle()
     check(out, *attention_ref(q, rows[None, :, None], v, 0.5, 0, None, dt), "far keys")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attention_keeps_nan_to_the_rows_that_see_it(dt, D):
+    B, Tq, Tk, H = 2, 150, 200, 2
+    q, k, v = rand(1, B, Tq, H, D, dt=dt), rand(2, B, Tk, H, D, dt=dt), rand(3, B, Tk, H, D, dt=dt)
+    ref, tol = attention_ref(q, k, v, 0.1, 1, None, dt)
+    q[0, 3, 0] = math.nan                                   # a query: its own row
+    k[1, 120, 1, 5] = math.nan                              # a key: the rows that see it (causal: from 70 on)
+    q[0, 9, 1, 0] = math.inf                                # infinite scores: the row
+    out = torch.empty_like(q)
+    gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, 0.1, 1, None, 0, out)
+    settle()
+    bad = torch.zeros(B, Tq, H, dtype=torch.bool, device="cuda")
+    bad[0, 3, 0] = bad[0, 9, 1] = True
+    bad[1, 70:, 1] = True
+    assert bool(torch.isnan(out[bad]).all())
+    check(out[~bad], ref[~bad], tol[~bad], "other rows")
 
 
 # ------------------------------------------------------------------ all of them
