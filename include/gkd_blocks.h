@@ -71,7 +71,7 @@ typedef struct gkd_heads {
  *   out       [T][Cout], rows out_stride apart, out_dt = GKD_BF16 or GKD_F32
  *             (dt = GKD_F32 takes GKD_F32 only). Columns past Cout are left alone.
  * dt = GKD_BF16: exact products, sums in fp32. dt = GKD_F32: every operand as a pair
- * of TF32 numbers, three products per term, each term within 2^-20 of its fp32
+ * of TF32 numbers, three products per term, each term within 2^-19 of its
  * product; x and weight must be finite (an infinity gives NaN). The epilogue is in
  * fp32, with one rounding to out_dt. `out` must not overlap x or weight.
  * Limits: 0 <= T < 2^31, 8 <= Cin, Cout <= 65536, both multiples of 8, strides

@@ -488,10 +488,11 @@ cudaError_t go(const AttentionArgs& a, unsigned work, int S, cudaStream_t stream
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
   using namespace att32;
   const long long work = (static_cast<long long>(a.Tq) + kRows - 1) / kRows * a.q.heads * a.B;
-  // few query tiles: a cluster shares the keys of one, while that keeps to one CTA per SM
+  // few query tiles: a cluster shares the keys of one, while that keeps to one CTA per SM (and to
+  // two thirds of them for clusters of 8, of which 16 run in two waves)
   const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + BN - 1) / BN);
   int S = 1;
-  while (S < 8 && work * S * 2 <= num_sms && ktiles >= 2 * S) S *= 2;
+  while (S < 8 && work * S * 2 <= (S == 4 ? 2 * num_sms / 3 : num_sms) && ktiles >= 2 * S) S *= 2;
   const unsigned w = static_cast<unsigned>(work);
   return a.D <= 64 ? go<1>(a, w, S, stream) : go<2>(a, w, S, stream);
 }

@@ -3,36 +3,40 @@
 //
 // Every operand is taken as x = hi + lo: hi is x without its low 13 bits (which
 // kind::tf32 does not read, so hi needs no copy), lo = x - hi rounded to TF32. Then
-// x w = hi hi + hi lo + lo hi to within 2^-20 of |x w|, three products per term, where
-// the fp32 units have a sixth of one product's rate.
+// x w = hi hi + hi lo + lo hi to within 2^-19 of |x w| (lo lo, below 2^-20, and twice
+// the rounding of lo), three products per term, where the fp32 units have a sixth of one
+// product's rate.
 // The tensor core truncates each step's sum, so a long sum drifts towards zero (at 1024
-// channels by 2.4e-6 of the result for plain TF32): the large products and the small
-// ones have accumulators of their own, and the epilogue warps add both up in fp32
-// after every 64 channels. Measured error at 1024 and 4096 channels: 2.9e-7 and 3.1e-7 of
-// the result (fp32 products by the library: 5.7e-7 and 1.1e-6).
-//
-// Measured (B200, in a graph): 1360 x 1024 -> 1024 35 us (64 x 64 tiles on the fp32 units
-// took 120), 80 rows 10.2 us. Bound by shared memory: a stage moves 160 KB through it (32
-// read and 32 written by the converters, 96 read by the products) where the products
-// alone would take 768 clocks.
+// channels by 2.4e-6 of the result for plain TF32): an accumulator holds 32 channels,
+// small products first, and warps of their own add the accumulators up in fp32. Measured
+// error: 2.4e-7 and 3.0e-7 of the result at 1024 and 4096 channels (fp32 products by the
+// library: 5.7e-7 and 1.1e-6).
 //
 // A CTA has a 128 x 128 tile of the output, 18 warps:
 //   warp 0       TMA: stages of 32 channels of x and of weight (128B-swizzled);
-//   warp 1       products, 12 per stage, into two pairs of accumulators in turn;
-//   warps 2-9    lo tiles: 16 bytes in, 16 bytes out at the same place of the next tile,
-//                whatever the swizzle;
+//   warp 1       products, 12 per stage, into two accumulators in turn;
+//   warps 2-5    x into tensor memory (a row per lane), as it is and its lo part;
+//   warps 6-9    lo parts of weight: 16 bytes in, 16 bytes out at the same place of the
+//                next tile, whatever the swizzle;
 //   warps 10-17  sums in registers (a thread: one row, 64 columns).
 // Few tiles: a cluster of S CTAs shares a tile's channels; the sums meet in shared
 // memory in rank order and every CTA finishes its share of the rows.
+//
+// Measured (B200, in a graph): 1360 x 1024 -> 1024 28 us, 80 rows 9.6 us, 9296 x 1280 -> 5120
+// 645 us = 189 TFLOP/s. 64 x 64 tiles on the fp32 units took 120 us for the first; both lo
+// parts in shared memory (160 KB through it per stage instead of 96), two accumulators of
+// 64 channels, 35. Bound by the stage's chain: some 1300 clocks where its products and
+// its shared-memory traffic need 768 each.
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
 namespace gkd {
 namespace lin32 {
 
-constexpr int kTile = 128, kChunk = 32, kStages = 3, kFlush = 2;   // stages per accumulator: 64 channels
+constexpr int kTile = 128, kChunk = 32, kStages = 4;
 constexpr int kOpBytes = kTile * 128;                              // one operand's tile of a stage
-constexpr int kStageBytes = 4 * kOpBytes;                          // x, weight, and their lo parts
+constexpr int kStageBytes = 3 * kOpBytes;                          // x, weight, weight's lo part
+constexpr uint32_t kColA = 256;                                    // accumulators at 0 and 128, x's stages (hi, lo) at 256 + 64 s
 constexpr int kConvWarps = 8, kSumWarps = 8, kThreads = 32 * (2 + kConvWarps + kSumWarps);
 
 struct Args {
@@ -133,23 +137,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
     // fp32 accumulator, tf32 x tf32, both K-major, M = N = 128
     constexpr uint32_t idesc = (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
     const uint64_t base = umma_desc_sw128(smem_u32(smem));
-    int it = 0, acc = 0;
+    int it = 0;
     for (; it < nk; ++it) {
-      const int s = it % kStages, buf = acc & 1;
-      const bool fresh = it % kFlush == 0;
-      if (fresh && acc >= 2 && !wait(&ctl->accempty[buf], ((acc >> 1) & 1) ^ 1)) break;
+      const int s = it % kStages, buf = it & 1;
+      if (it >= 2 && !wait(&ctl->accempty[buf], ((it >> 1) & 1) ^ 1)) break;
       if (!wait(&ctl->ready[s], (it / kStages) & 1)) break;
       tc_fence_after();
-      const uint64_t x = base + ((s * kStageBytes) >> 4), w = x + (kOpBytes >> 4), xl = w + (kOpBytes >> 4), wl = xl + (kOpBytes >> 4);
-      const uint32_t big = tmem + 256 * buf, small = big + 128;
-      umma_ss_tf32_x4_elect(small, x, wl, idesc, fresh ? 0u : 1u);
-      umma_ss_tf32_x4_elect(small, xl, w, idesc, 1u);
-      umma_ss_tf32_x4_elect(big, x, w, idesc, fresh ? 0u : 1u);
+      const uint64_t w = base + ((s * kStageBytes + kOpBytes) >> 4), wl = w + (kOpBytes >> 4);
+      const uint32_t d = tmem + 128 * buf, hi = tmem + kColA + 64 * s, lo = hi + 32;
+      umma_ts_tf32_x4_elect(d, hi, wl, idesc, 0u);                 // small products first
+      umma_ts_tf32_x4_elect(d, lo, w, idesc, 1u);
+      umma_ts_tf32_x4_elect(d, hi, w, idesc, 1u);
       umma_commit_elect(&ctl->empty[s]);
-      if (it % kFlush == kFlush - 1 || it == nk - 1) {
-        umma_commit_elect(&ctl->accfull[buf]);
-        ++acc;
-      }
+      umma_commit_elect(&ctl->accfull[buf]);
     }
     if (!ok) give_up();
     if (it > 0) {                                                  // what was issued ends before the CTA does
@@ -157,16 +157,44 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
       if (!mbar_wait_drain(&ctl->drain, 0, lim) && lane == 0) atomicOr(a.err, kErrTimeout);
     }
     __syncwarp();
+  } else if (warp < 6) {
+    // x: a row per lane of tensor memory, as it is (hi) and its lo part
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t dst = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColA;
+    for (int it = 0; it < nk; ++it) {
+      const int s = it % kStages;
+      if (!wait(&ctl->full[s], (it / kStages) & 1)) break;         // the last products that read the stage have ended
+      const uint8_t* p = smem + s * kStageBytes + r * 128;
+      uint32_t hi[32], lo[32];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(p + ((c ^ (r & 7)) << 4));
+        hi[4 * c] = __float_as_uint(v.x);
+        hi[4 * c + 1] = __float_as_uint(v.y);
+        hi[4 * c + 2] = __float_as_uint(v.z);
+        hi[4 * c + 3] = __float_as_uint(v.w);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) lo[c] = __float_as_uint(lo_part(__uint_as_float(hi[c])));
+      tmem_st_32x32b_x32(dst + 64 * s, hi);
+      tmem_st_32x32b_x32(dst + 64 * s + 32, lo);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ready[s]);
+    }
+    if (!ok) give_up();
   } else if (warp < 2 + kConvWarps) {
-    const int tid = threadIdx.x - 64;
+    // weight: lo parts, 16 bytes in, 16 bytes out at the same place of the next tile
+    const int tid = threadIdx.x - 32 * 6;
     for (int it = 0; it < nk; ++it) {
       const int s = it % kStages;
       if (!wait(&ctl->full[s], (it / kStages) & 1)) break;
-      uint8_t* p = smem + s * kStageBytes + tid * 16;
+      uint8_t* p = smem + s * kStageBytes + kOpBytes + tid * 16;
 #pragma unroll
-      for (int i = 0; i < 2 * kOpBytes / (16 * 32 * kConvWarps); ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(p + i * (16 * 32 * kConvWarps));
-        *reinterpret_cast<float4*>(p + i * (16 * 32 * kConvWarps) + 2 * kOpBytes) =
+      for (int i = 0; i < kOpBytes / (16 * 128); ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + i * (16 * 128));
+        *reinterpret_cast<float4*>(p + i * (16 * 128) + kOpBytes) =
             make_float4(lo_part(v.x), lo_part(v.y), lo_part(v.z), lo_part(v.w));
       }
       fence_proxy_async_smem();
@@ -180,19 +208,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
     float v[64];
 #pragma unroll
     for (int j = 0; j < 64; ++j) v[j] = 0.f;
-    for (int k0 = 0, acc = 0; k0 < nk; k0 += kFlush, ++acc) {
-      const int buf = acc & 1;
-      if (!wait(&ctl->accfull[buf], (acc >> 1) & 1)) break;
+    for (int it = 0; it < nk; ++it) {
+      const int buf = it & 1;
+      if (!wait(&ctl->accfull[buf], (it >> 1) & 1)) break;
       tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        uint32_t big[8], small[8];
-        tmem_ld_32x32b_x8(src0 + 256 * buf + 8 * g, big);
-        tmem_ld_32x32b_x8(src0 + 256 * buf + 128 + 8 * g, small);
-        tmem_wait_ld_regs(big);
-        tmem_wait_ld_regs(small);
+      for (int g = 0; g < 4; ++g) {
+        uint32_t d[16];
+        tmem_ld_32x32b_x16(src0 + 128 * buf + 16 * g, d);
+        tmem_wait_ld_regs(d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * g + j] += __uint_as_float(big[j]) + __uint_as_float(small[j]);
+        for (int j = 0; j < 16; ++j) v[16 * g + j] += __uint_as_float(d[j]);
       }
       tc_fence_before();
       __syncwarp();
@@ -269,8 +295,11 @@ cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t str
   p.wait_limit_ns = a.wait_limit_ns;
   const long long tiles = (static_cast<long long>(a.T) + kTile - 1) / kTile * ((a.Cout + kTile - 1) / kTile);
   const int nk = (a.Cin + kChunk - 1) / kChunk;
+  // Few tiles: the channels are split, up to one CTA per SM; clusters of 8 up to two thirds of
+  // that, since a group of SMs that shares clusters has places left over (16 clusters of 8 ran
+  // in two waves: 17 x 1280 -> 2048 took 19.1 us, with clusters of 4 13.1).
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= num_sms && nk >= 4 * S) S *= 2;
+  while (S < 8 && tiles * S * 2 <= (S == 4 ? 2 * num_sms / 3 : num_sms) && nk >= 4 * S) S *= 2;
   cudaError_t e = allow_smem<linear_f32_kernel>(kSmem);
   if (e != cudaSuccess) return e;
   return launch_cluster(linear_f32_kernel, dim3(static_cast<unsigned>(tiles * S)), kThreads, kSmem, S, stream, p, S);

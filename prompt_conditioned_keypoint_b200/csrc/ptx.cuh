@@ -327,19 +327,20 @@ __device__ __forceinline__ void umma_ss_f16_x4_elect(uint32_t d_tmem, uint64_t a
       : "memory");
 }
 
-// The same for kind::tf32 (fp32 operands read as TF32): four K = 8 steps of one 32-channel chunk.
-__device__ __forceinline__ void umma_ss_tf32_x4_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+// Four K = 8 steps of one 32-channel chunk of kind::tf32 (fp32 operands read as TF32), A in
+// tensor memory (8 columns apart), B in shared memory (descriptors 32 bytes apart).
+__device__ __forceinline__ void umma_ts_tf32_x4_elect(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
                                                       uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q, e;\n\t"
       "setp.ne.b32 p, %10, 0;\n\t"
       "setp.eq.b32 q, %10, %10;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %5, %9, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], %2, %6, %9, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], %3, %7, %9, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], %4, %8, %9, q;\n\t}"
-      ::"r"(d_tmem), "l"(a), "l"(a + 2), "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc),
+      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %5, %9, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], [%2], %6, %9, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], [%3], %7, %9, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], [%4], %8, %9, q;\n\t}"
+      ::"r"(d_tmem), "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc),
         "r"(accumulate)
       : "memory");
 }
@@ -486,13 +487,6 @@ __device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                  "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&v)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
                :
                : "memory");
 }
