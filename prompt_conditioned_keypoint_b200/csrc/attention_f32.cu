@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     // ---------------------------------------------------------------- softmax: one row per thread
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const bool active = r0 + 32 * q < a.Tq;
     float m = -INFINITY, l = 0.f, acc[64 * DCH];
 #pragma unroll
     for (int e = 0; e < 64 * DCH; ++e) acc[e] = 0.f;
@@ -285,6 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       }
       if (!wait(&ctl->sfull[j & 1], (j >> 1) & 1)) break;
       tc_fence_after();
+      if (!active) {                                // no row inside Tq: barriers alone
+        if (j > 0 && !wait(&ctl->odone[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->pready[j & 1]);
+        continue;
+      }
       float x[BN];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         if (!ok) break;
       }
     }
-    if (ok && j > 0) gather(j - 1, 1.f);
+    if (ok && j > 0 && active) gather(j - 1, 1.f);
     if (!ok) give_up();
     if (S == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / l;

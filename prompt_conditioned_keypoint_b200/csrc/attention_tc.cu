@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int ochunks = (a.D + 15) / 16;
+    // A warp without a row inside Tq keeps to the barriers: what its lanes of tensor memory hold meets no other row.
+    const bool active = r0 + 32 * q < a.Tq;
     float m = -INFINITY, l = 0.f;                   // the maximum that the weights are taken against, their sum
     uint32_t j = 0;
     bool ok = true;
@@ -357,95 +359,97 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       if (!wait(&ctl->sfull[j % kBufs], (j / kBufs) & 1)) break;
       tc_fence_after();
       const uint32_t scores = lane_base + 64 * (j % kBufs);
-      // Hidden keys: -inf over their scores first, so that what follows is the same code
-      // without tests for every tile. (With the tests inside it 8 x 2309 rows took 386 us
-      // against 344; a second copy of it for whole tiles took 335, but 80 x 77 causal rows
-      // under a mask 35.8 against 30.9.)
-      if (!plain) {
+      if (active) {
+        // Hidden keys: -inf over their scores first, so that what follows is the same code
+        // without tests for every tile. (With the tests inside it 8 x 2309 rows took 386 us
+        // against 344; a second copy of it for whole tiles took 335, but 80 x 77 causal rows
+        // under a mask 35.8 against 30.9.)
+        if (!plain) {
 #pragma unroll 1
-        for (int g = 0; g < 2 * W; ++g) {
-          uint32_t x[16] = {};
-          if (g < 2 * words) {
-            tmem_ld_32x32b_x16(scores + 16 * g, x);
-            tmem_wait_ld_regs(x);
-          }
-          const uint32_t b16 = (g < 2 ? bits[0] : bits[1]) >> (16 * (g & 1));
+          for (int g = 0; g < 2 * W; ++g) {
+            uint32_t x[16] = {};
+            if (g < 2 * words) {
+              tmem_ld_32x32b_x16(scores + 16 * g, x);
+              tmem_wait_ld_regs(x);
+            }
+            const uint32_t b16 = (g < 2 ? bits[0] : bits[1]) >> (16 * (g & 1));
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;
-          tmem_st_32x32b_x16(scores + 16 * g, x);
+            for (int e = 0; e < 16; ++e)
+              if (!((b16 >> e) & 1u)) x[e] = 0xff800000u;
+            tmem_st_32x32b_x16(scores + 16 * g, x);
+          }
+          tmem_wait_st();
         }
+        // Groups of 16 scores. With two CTAs per SM a tile's scores stay in registers; with
+        // four they are read twice, for the maximum and for the weights, and a group is on
+        // its way while the one before is worked on.
+        uint32_t v[kHold ? 2 * W : 2][16];
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto load = [&](int g) { tmem_ld_32x32b_x16(scores + 16 * g, v[kHold ? g : g & 1]); };
+        load(0);
+        if (kHold) {
+#pragma unroll
+          for (int g = 1; g < 2 * W; ++g) load(g);
+        }
+#pragma unroll
+        for (int g = 0; g < 2 * W; ++g) {
+          uint32_t(&x)[16] = v[kHold ? g : g & 1];
+          tmem_wait_ld_regs(x);
+          if (!kHold && g + 1 < 2 * W) load(g + 1);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        }
+        const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);   // NaN if any score is
+        const bool grow = !((top - m) * a.scale_log2 <= kGrow);   // also for NaN, and where there was no key before
+        if (__any_sync(0xffffffffu, grow)) {
+          float mn = max3_nan(m, top, top);
+          if (mn == INFINITY) mn = NAN;               // infinity against infinity: the row is NaN
+          const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
+          m = mn;
+          l *= f;
+          if (j > 0) {
+            // O is at rest: the product before the last ended before these scores were
+            // formed, and with one buffer the last one did too
+            if (kBufs == 2 && !wait(&ctl->pvdone, (j - 1) & 1)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < ochunks; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(lane_base + kColO + 16 * c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), base2 = make_float2(-base, -base);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (!kHold) load(0);
+#pragma unroll
+        for (int g = 0; g < 2 * W; ++g) {
+          uint32_t(&x)[16] = v[kHold ? g : g & 1];
+          if (!kHold) {
+            tmem_wait_ld_regs(x);
+            if (g + 1 < 2 * W) load(g + 1);
+          }
+          uint32_t p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, base2);
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            p[e] = pack_bf16x2(y.x, y.y);
+          }
+          tmem_st_32x32b_x8(scores + 8 * g, p);       // over scores that are done with: 8 g + 8 <= 16 g + 16
+        }
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
         tmem_wait_st();
       }
-      // Groups of 16 scores. With two CTAs per SM a tile's scores stay in registers; with
-      // four they are read twice, for the maximum and for the weights, and a group is on
-      // its way while the one before is worked on.
-      uint32_t v[kHold ? 2 * W : 2][16];
-      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto load = [&](int g) { tmem_ld_32x32b_x16(scores + 16 * g, v[kHold ? g : g & 1]); };
-      load(0);
-      if (kHold) {
-#pragma unroll
-        for (int g = 1; g < 2 * W; ++g) load(g);
-      }
-#pragma unroll
-      for (int g = 0; g < 2 * W; ++g) {
-        uint32_t(&x)[16] = v[kHold ? g : g & 1];
-        tmem_wait_ld_regs(x);
-        if (!kHold && g + 1 < 2 * W) load(g + 1);
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-      }
-      const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);   // NaN if any score is
-      const bool grow = !((top - m) * a.scale_log2 <= kGrow);   // also for NaN, and where there was no key before
-      if (__any_sync(0xffffffffu, grow)) {
-        float mn = max3_nan(m, top, top);
-        if (mn == INFINITY) mn = NAN;               // infinity against infinity: the row is NaN
-        const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
-        m = mn;
-        l *= f;
-        if (j > 0) {
-          // O is at rest: the product before the last ended before these scores were
-          // formed, and with one buffer the last one did too
-          if (kBufs == 2 && !wait(&ctl->pvdone, (j - 1) & 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < ochunks; ++c) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(lane_base + kColO + 16 * c, o);
-            tmem_wait_ld_regs(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_32x32b_x16(lane_base + kColO + 16 * c, o);
-          }
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
-      const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), base2 = make_float2(-base, -base);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      if (!kHold) load(0);
-#pragma unroll
-      for (int g = 0; g < 2 * W; ++g) {
-        uint32_t(&x)[16] = v[kHold ? g : g & 1];
-        if (!kHold) {
-          tmem_wait_ld_regs(x);
-          if (g + 1 < 2 * W) load(g + 1);
-        }
-        uint32_t p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, base2);
-          y.x = ex2_approx(y.x);
-          y.y = ex2_approx(y.y);
-          sum[e & 1] = add2(sum[e & 1], y);
-          p[e] = pack_bf16x2(y.x, y.y);
-        }
-        tmem_st_32x32b_x8(scores + 8 * g, p);       // over scores that are done with: 8 g + 8 <= 16 g + 16
-      }
-      sum[0] = add2(sum[0], sum[1]);
-      l += sum[0].x + sum[0].y;
-      tmem_wait_st();
       if (MASK && !plain) {                         // rows of V that no row may see
         const uint32_t s = j % kKvStages;
         if (!wait(&ctl->vfull[s], (j / kKvStages) & 1)) break;
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       ctl->m[r] = m;
       ctl->l[r] = l;
     }
-    for (int c = 0; c < ochunks; ++c) {
+    for (int c = 0; active && c < ochunks; ++c) {
       uint32_t v[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] = 0u;

@@ -248,10 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
     float4 b = make_float4(0.f, 0.f, 0.f, 0.f), sc = make_float4(1.f, 1.f, 1.f, 1.f);
     if (a.bias) b = *reinterpret_cast<const float4*>(a.bias + c);
     if (a.scale) sc = *reinterpret_cast<const float4*>(a.scale + c);
-    for (int r = rank * (kTile / S) + warp; r < (rank + 1) * (kTile / S) && t0 + r < a.T; r += kThreads / 32) {
-      const long long t = t0 + r;
-      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.residual) res = load4(a.residual + t * a.residual_stride + c);
+    // a warp's rows, their residuals in flight together
+    constexpr int kMine = (kTile + kThreads / 32 - 1) / (kThreads / 32);
+    const int last = min((rank + 1) * (kTile / S), a.T - t0);
+    auto row = [&](int i) { return rank * (kTile / S) + warp + i * (kThreads / 32); };
+    float4 res[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      res[i] = a.residual && row(i) < last ? load4(a.residual + static_cast<long long>(t0 + row(i)) * a.residual_stride + c)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int r = row(i);
+      if (r >= last) break;
       const uint32_t at = r * 512 + ((lane ^ (r & 31)) << 4);
       float z[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll 8
@@ -263,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
         z[3] += v.w;
       }
       activate(z, a.act);
-      store4(a.out + t * a.out_stride + c, make_float4(fmaf(sc.x, z[0], res.x), fmaf(sc.y, z[1], res.y),
-                                                       fmaf(sc.z, z[2], res.z), fmaf(sc.w, z[3], res.w)));
+      store4(a.out + static_cast<long long>(t0 + r) * a.out_stride + c,
+             make_float4(fmaf(sc.x, z[0], res[i].x), fmaf(sc.y, z[1], res[i].y), fmaf(sc.z, z[2], res[i].z),
+                         fmaf(sc.w, z[3], res[i].w)));
     }
   }
   __syncwarp();

@@ -484,25 +484,34 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     float4 b = make_float4(0.f, 0.f, 0.f, 0.f), sc = make_float4(1.f, 1.f, 1.f, 1.f);
     if (a.bias) b = *reinterpret_cast<const float4*>(a.bias + c);
     if (a.scale) sc = *reinterpret_cast<const float4*>(a.scale + c);
-    for (int n = rank * (N / S) + warp; n < (rank + 1) * (N / S) && t0 + n < a.T; n += kSplitThreads / 32) {
-      const long long t = t0 + n;
-      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.residual) res = load4(static_cast<const TO*>(a.residual) + t * a.residual_stride + c);
-      float4 y = b;
+    // a warp's rows, their residuals in flight together
+    constexpr int kMine = (N + kSplitThreads / 32 - 1) / (kSplitThreads / 32);
+    const int last = min((rank + 1) * (N / S), a.T - t0);
+    auto row = [&](int i) { return rank * (N / S) + warp + i * (kSplitThreads / 32); };
+    float4 res[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      res[i] = a.residual && row(i) < last
+                   ? load4(static_cast<const TO*>(a.residual) + static_cast<long long>(t0 + row(i)) * a.residual_stride + c)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int n = row(i);
+      if (n >= last) break;
+      float z[4] = {b.x, b.y, b.z, b.w};
       const uint32_t at = base + (n * 128 + 4 * lane) * 4;
 #pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float4 v = S > 1 ? cluster_load4(cluster_map(at, s)) : *reinterpret_cast<const float4*>(part + n * 128 + 4 * lane);
-        y.x += v.x;
-        y.y += v.y;
-        y.z += v.z;
-        y.w += v.w;
+        z[0] += v.x;
+        z[1] += v.y;
+        z[2] += v.z;
+        z[3] += v.w;
       }
-      float z[4] = {y.x, y.y, y.z, y.w};
       activate(z, a.act);
-      store4(static_cast<TO*>(a.out) + t * a.out_stride + c,
-             make_float4(fmaf(sc.x, z[0], res.x), fmaf(sc.y, z[1], res.y), fmaf(sc.z, z[2], res.z),
-                         fmaf(sc.w, z[3], res.w)));
+      store4(static_cast<TO*>(a.out) + static_cast<long long>(t0 + n) * a.out_stride + c,
+             make_float4(fmaf(sc.x, z[0], res[i].x), fmaf(sc.y, z[1], res[i].y), fmaf(sc.z, z[2], res[i].z),
+                         fmaf(sc.w, z[3], res[i].w)));
     }
   }
   __syncwarp();
