@@ -21,6 +21,8 @@
  * first tensor argument, no allocation, no synchronisation, gkd_status codes,
  * gkd_last_error(), 16-byte alignment of tensor base pointers and byte strides.
  * A call whose outputs would be empty returns GKD_OK and launches nothing.
+ * Waits inside the kernels have gkd.h's limit (gkd_set_wait_timeout_ms) and report to
+ * its error word (gkd_check_device_error).
  * Outputs may be used on another stream once that stream waits for `stream`.
  * No call keeps state between calls: calls may run at once on any streams, and
  * captured calls may be replayed in any order. Results do not depend on
@@ -124,7 +126,9 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  *   p_j = exp(scale * q[b,i,h,:] . k[b,j,g,:] - max_j'(...)),   g = h * k->heads / q->heads
  * over the keys j with key_mask[b,j] != 0 (all, if NULL) and, if causal,
  * j <= i + Tk - Tq (the last query sees every key). Rows without such a key are 0.
- * Keys and values that the key mask hides may hold anything, NaN included.
+ * Keys and values that the key mask hides may hold anything, NaN included. A NaN or an
+ * infinity in a value v[b,j] that the mask does not hide can reach any row of its batch
+ * and head, also one that the diagonal keeps from key j.
  *
  *   q        [B][Tq] rows of q->heads heads of D elements, type dt
  *   k, v     [B][Tk] rows; k->heads == v->heads divides q->heads

@@ -31,7 +31,8 @@ namespace att32 {
 
 constexpr int kThreads = 512, kRows = 128, BN = 64, W = 2, kInfo = 4, kConvThreads = 256;
 // 512 threads have 128 registers each; the softmax warps hold a row of scores and one of outputs:
-// 64 + 240 + 2 x 104 <= 4 x 128.
+// 64 + 240 + 2 x 104 <= 4 x 128. Each group changes its share once, at the start of its role: a second
+// change would need the group's warps to meet before it.
 constexpr int kRegsIssue = 64, kRegsSoft = 240, kRegsConv = 104;
 
 struct Info {                                       // one key tile
@@ -454,8 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
   if (S > 1) {
     cluster_sync();
     const uint32_t om = smem_u32(ctl->m), ol = smem_u32(ctl->l), oo = smem_u32(qs);
+    // by the softmax warps, which have the registers for it: the others keep to the barriers from here
     const int pieces = a.D / 4, share = kRows / S;
-    for (int i = threadIdx.x; i < share * pieces; i += kThreads) {
+    for (int i = warp >= 4 && warp < 8 ? threadIdx.x - 128 : share * pieces; i < share * pieces; i += 128) {
       const int r = rank * share + i / pieces, c = i % pieces;
       if (r0 + r >= a.Tq) continue;
       float top = -INFINITY;                        // loops without branches: the loads are in flight together
