@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       }
     }
     if (ok && j > 0 && active) gather(j - 1, 1.f);
+    if (S > 1 && j == 0) wait(&ctl->qready, 0);     // no tile: Q's planes, which the share overwrites, may still be written
     if (!ok) give_up();
     if (S == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
             store4(o + 4 * c, make_float4(acc[4 * c] * inv, acc[4 * c + 1] * inv, acc[4 * c + 2] * inv, acc[4 * c + 3] * inv));
       }
     } else {
-      // this CTA's share, over Q's planes (their last reader is done): row r's 16-byte pieces c at c ^ (r & 15)
+      // this CTA's share, over Q's planes (written, and their last reader is done): row r's 16-byte pieces c at c ^ (r & 15)
       ctl->m[r] = m;
       ctl->l[r] = l;
 #pragma unroll

@@ -457,6 +457,32 @@ def test_attention_keeps_nan_to_the_rows_that_see_it(dt, D):
     check(out[~bad], ref[~bad], tol[~bad], "other rows")
 
 
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [0, 1])
+def test_attention_keeps_nan_to_its_row_where_shares_have_no_key(dt, D, causal):
+    """Fewer key tiles than the CTAs that share a query tile (the first rows of a causal call, a mask that
+    leaves the first keys): a share without a key adds nothing to any row, whatever Q holds."""
+    B, T, H = 1, 1024, 2
+    q, k, v = rand(11, B, T, H, D, dt=dt), rand(12, B, T, H, D, dt=dt), rand(13, B, T, H, D, dt=dt)
+    mask = None
+    if not causal:
+        mask = torch.zeros(B, T, dtype=torch.uint8, device="cuda")
+        mask[:, :40] = 1
+    ref, tol = attention_ref(q, k, v, 0.1, causal, mask, dt)
+    bad = torch.zeros(B, T, H, dtype=torch.bool, device="cuda")
+    for first in (5, 64, 127, 300):
+        q[:, first] = math.nan
+        q[:, first + 3, :, ::2] = math.inf
+        bad[:, first] = bad[:, first + 3] = True
+    for _ in range(20):
+        out = torch.full_like(q, 7.0)
+        gk.gkd_attention(q, k, v, DT[dt][1], B, T, T, D, 0.1, causal, mask, T if mask is not None else 0, out)
+        settle()
+        assert bool(torch.isnan(out[bad]).all())
+        check(out[~bad], ref[~bad], tol[~bad], "other rows")
+
+
 # ------------------------------------------------------------------ all of them
 def ours(seed, dt, T):
     """One pass of each operator on fresh buffers; returns a callable and its outputs."""
