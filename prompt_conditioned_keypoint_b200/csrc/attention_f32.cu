@@ -1,5 +1,6 @@
-// gkd_attention for fp32 on the tensor cores: out = softmax(scale q k^T) v under a key
-// mask, with fp32 accuracy from bf16 products.
+// gkd_attention for fp32: out = softmax(scale q k^T) v under a key mask. Two kernels: one on
+// the tensor cores, with fp32 accuracy from bf16 products, which this comment describes, and
+// one on the fma units for up to 24 keys, below.
 //
 // Every operand is taken as x = b0 + b1 + b2, b0 = bf16(x), b1 = bf16(x - b0), b2 =
 // bf16(x - b0 - b1): 24 bits. Of the nine products per term the six with i + j <= 2 are
@@ -496,7 +497,159 @@ cudaError_t go(const AttentionArgs& a, unsigned work, int S, cudaStream_t stream
 
 }  // namespace att32
 
+// Up to 24 keys: scores, softmax and output by fp32 fmas. The tensor-core kernel's CTA, one per SM, spends
+// such a call on its set-up; here a CTA of 64 rows needs about 100 registers a thread, so that four or more
+// share an SM. Four lanes share a row (16-byte pieces l, l + 4, .. each: a row's loads and stores fill whole
+// sectors), a thread has two rows and keeps their scores in registers; K and V, zeros where hidden, lie in
+// shared memory, and a read of 64 bytes of it serves the warp's 16 rows. Two shuffles add up a score.
+// Bound by HBM at a few keys, by those reads from 16 on. Measured (B200, us, keys 3 / 8 / 16 / 24, the
+// tensor-core kernel in brackets): 54 x 131 rows of 20 heads of 64 20.6 / 27.1 / 42.4 / 61.2 (122 to 123),
+// 4 x 1024 rows of 8 heads of 128 7.7 / 9.9 / 18.7 / 24.5 (25), 2304 rows of 16 heads of 64
+// 5.3 / 6.4 / 9.2 / 12.0 (17.6), one row of 16 heads of 128 4.1 / 4.8 / 6.8 / 9.0 (10). At 32 keys it took
+// 85 (123), 31 (25), 20 (17.7) and 11.2 (10).
+namespace att32few {
+
+constexpr int kThreads = 128, R = 2, kRows = R * kThreads / 4;
+
+template <int NP, int KMAX>                         // 16-byte pieces of a row per lane: D <= 16 NP; Tk <= KMAX
+__global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __grid_constant__ AttentionArgs a) {
+  __shared__ float4 ks[KMAX * 4 * NP], vs[KMAX * 4 * NP];
+  const int ntiles = static_cast<int>((static_cast<long long>(a.Tq) + kRows - 1) / kRows);
+  const int tile = blockIdx.x % ntiles, bh = blockIdx.x / ntiles;
+  const int h = bh % a.q.heads, b = bh / a.q.heads, hk = h / (a.q.heads / a.k.heads);
+  const int lane = threadIdx.x & 31, l4 = lane & 3, nq4 = a.D / 4;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* q = static_cast<const float*>(a.q.data) + b * a.q.batch_stride + h * a.q.head_stride;
+  const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
+  const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
+
+  // every load before the first use of one
+  const uint8_t mine = lane < a.Tk ? (mask ? mask[lane] : 1) : 0;
+  constexpr int kPieces = (KMAX * 4 * NP + kThreads - 1) / kThreads;
+  float4 kr[kPieces], vr[kPieces];
+#pragma unroll
+  for (int n = 0; n < kPieces; ++n) {
+    const int i = threadIdx.x + n * kThreads, j = i / (4 * NP), c = i % (4 * NP);
+    kr[n] = j < a.Tk && c < nq4 ? load4(k + j * a.k.row_stride + 4 * c) : zero;
+    vr[n] = j < a.Tk && c < nq4 ? load4(v + j * a.v.row_stride + 4 * c) : zero;
+  }
+  long long row[R];
+  float4 x[R][NP];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    row[i] = static_cast<long long>(tile) * kRows + i * (kThreads / 4) + (threadIdx.x >> 2);
+#pragma unroll
+    for (int c = 0; c < NP; ++c)
+      x[i][c] = row[i] < a.Tq && 4 * c + l4 < nq4 ? load4(q + row[i] * a.q.row_stride + 4 * (4 * c + l4)) : zero;
+  }
+  const uint32_t seen = __ballot_sync(0xffffffffu, mine != 0);
+#pragma unroll
+  for (int n = 0; n < kPieces; ++n) {
+    const int i = threadIdx.x + n * kThreads;
+    const bool live = (seen >> ((i / (4 * NP)) & 31)) & 1u;        // a hidden key's row becomes zeros
+    if (i < KMAX * 4 * NP) {
+      ks[i] = live ? kr[n] : zero;
+      vs[i] = live ? vr[n] : zero;
+    }
+  }
+  __syncthreads();
+
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+  float w[R][KMAX], inv[R];
+#pragma unroll
+  for (int j0 = 0; j0 < KMAX; j0 += 4) {            // four keys at a time: their sums in flight together
+#pragma unroll
+    for (int j = j0; j < j0 + 4; ++j)
+#pragma unroll
+      for (int i = 0; i < R; ++i) w[i][j] = 0.f;
+    if (j0 >= a.Tk) continue;
+#pragma unroll
+    for (int c = 0; c < NP; ++c)
+#pragma unroll
+      for (int j = j0; j < j0 + 4; ++j) {
+        const float4 y = ks[j * 4 * NP + 4 * c + l4];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          w[i][j] = fmaf(x[i][c].x, y.x, fmaf(x[i][c].y, y.y, fmaf(x[i][c].z, y.z, fmaf(x[i][c].w, y.w, w[i][j]))));
+      }
+#pragma unroll
+    for (int m = 1; m <= 2; ++m)
+#pragma unroll
+      for (int j = j0; j < j0 + 4; ++j)
+#pragma unroll
+        for (int i = 0; i < R; ++i) w[i][j] += __shfl_xor_sync(0xffffffffu, w[i][j], m);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    uint32_t bits = seen;
+    if (a.causal) {                                 // keys up to the diagonal
+      const int n = static_cast<int>(max(0ll, min(row[i] + a.Tk - a.Tq + 1, 32ll)));
+      bits &= n == 32 ? 0xffffffffu : (1u << n) - 1u;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < KMAX; j += 2) {
+      w[i][j] = (bits >> j) & 1u ? w[i][j] : -INFINITY;
+      w[i][j + 1] = (bits >> (j + 1)) & 1u ? w[i][j + 1] : -INFINITY;
+      top = max3_nan(top, w[i][j], w[i][j + 1]);    // NaN if any score was
+    }
+    const float base = top == -INFINITY ? 0.f : top * scale_log2;   // no key: every weight is 0
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      w[i][j] = ex2_approx(fmaf(w[i][j], scale_log2, -base));
+      sum[j & 3] += w[i][j];
+    }
+    const float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    inv[i] = l == 0.f ? 0.f : 1.f / l;
+  }
+#pragma unroll
+  for (int c = 0; c < NP; ++c) {
+    float4 o[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) o[i] = zero;
+#pragma unroll
+    for (int j0 = 0; j0 < KMAX; j0 += 4) {
+      if (j0 >= a.Tk) continue;
+#pragma unroll
+      for (int j = j0; j < j0 + 4; ++j) {
+        const float4 y = vs[j * 4 * NP + 4 * c + l4];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          o[i] = make_float4(fmaf(w[i][j], y.x, o[i].x), fmaf(w[i][j], y.y, o[i].y), fmaf(w[i][j], y.z, o[i].z),
+                             fmaf(w[i][j], y.w, o[i].w));
+      }
+    }
+    if (4 * c + l4 >= nq4) continue;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (row[i] < a.Tq)
+        store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + row[i] * a.out.row_stride + h * a.out.head_stride +
+                   4 * (4 * c + l4),
+               make_float4(o[i].x * inv[i], o[i].y * inv[i], o[i].z * inv[i], o[i].w * inv[i]));
+  }
+}
+
+template <int NP, int KMAX>
+cudaError_t go(const AttentionArgs& a, cudaStream_t stream) {
+  const long long work = (static_cast<long long>(a.Tq) + kRows - 1) / kRows * a.q.heads * a.B;   // fits: the caller's check
+  attention_few_keys_kernel<NP, KMAX><<<static_cast<unsigned>(work), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int KMAX>
+cudaError_t go(const AttentionArgs& a, cudaStream_t stream) {
+  return a.D <= 64 ? go<4, KMAX>(a, stream) : go<8, KMAX>(a, stream);
+}
+
+}  // namespace att32few
+
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
+  // few keys: fma units, above 24 tensor cores (both sides beside that kernel)
+  if (a.Tk <= 8) return att32few::go<8>(a, stream);
+  if (a.Tk <= 16) return att32few::go<16>(a, stream);
+  if (a.Tk <= 24) return att32few::go<24>(a, stream);
   using namespace att32;
   const long long work = (static_cast<long long>(a.Tq) + kRows - 1) / kRows * a.q.heads * a.B;
   // few query tiles: a cluster shares the keys of one, while that keeps to one CTA per SM (and to

@@ -370,6 +370,15 @@ def attention_case(case, seed=21):
     return q, k, v, masks(kind, seed + 3, B, Tk)
 
 
+# few keys: each size of that kernel and both sides of it, rows behind a tile, shared heads, more queries than keys
+ATTENTION += [(2, q, k, 4, hk, D, "f32", causal, kind)
+              for q, k, hk, D, causal, kind in [
+                  (1, 1, 4, 64, 0, "prefix"), (65, 2, 2, 8, 0, "holes"), (131, 3, 2, 64, 0, "all"), (64, 7, 4, 24, 0, "last"),
+                  (200, 8, 1, 128, 1, "all"), (33, 9, 4, 72, 0, "holes"), (17, 16, 4, 16, 1, "holes"), (17, 17, 2, 64, 1, "prefix"),
+                  (300, 17, 4, 104, 0, "holes"), (5, 24, 1, 128, 1, "prefix"), (129, 24, 4, 64, 0, "all"), (129, 25, 4, 64, 0, "all"),
+                  (40, 32, 2, 64, 1, "holes"), (70, 33, 4, 128, 0, "holes")]]
+
+
 @pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "-".join(str(v) for v in c))
 def test_attention(case):
     B, Tq, Tk, H, Hk, D, dt, causal, kind = case
@@ -436,6 +445,45 @@ def test_attention_keys_past_32_bit_offsets(dt):
     gk.gkd_attention(q, k, v, DT[dt][1], 1, 3, Tk, D, 0.5, 0, None, 0, out)
     settle()
     check(out, *attention_ref(q, rows[None, :, None], v, 0.5, 0, None, dt), "far keys")
+
+
+def test_attention_many_keys_past_32_bit_offsets():
+    Tk, D, stride = 30, 64, 2 ** 27 + 64
+    buf = torch.empty((Tk - 1) * stride + D, device="cuda")
+    rows, k = rand(1, Tk, D, dt="f32"), rand(2, 1, Tk, 1, D, dt="f32")
+    v = buf.as_strided((1, Tk, 1, D), (0, stride, D, 1))
+    v[0, :, 0] = rows
+    q, out = rand(3, 1, 3, 1, D, dt="f32", std=3.0), torch.empty(1, 3, 1, D, device="cuda")
+    gk.gkd_attention(q, k, v, DT["f32"][1], 1, 3, Tk, D, 0.5, 0, None, 0, out)
+    settle()
+    check(out, *attention_ref(q, k, rows[None, :, None], 0.5, 0, None, "f32"), "far values")
+
+
+@pytest.mark.parametrize("Tk", [3, 16, 24])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attention_over_few_keys_on_slices_with_nan(dt, Tk):
+    """Strided views and one set of keys for all batches; NaN and infinities reach only the rows that meet them."""
+    B, Tq, H, D = 3, 70, 4, 64
+    base = rand(1, B, Tq + 3, H + 2, D + 16, dt=dt)
+    q = base[:, 2:Tq + 2, 1:H + 1, 8:D + 8]
+    kv = rand(2, 1, 2, H, Tk, D, dt=dt)                                             # heads outside, rows inside
+    k, v = (kv[:, i].transpose(1, 2)[:, :, :2].expand(B, -1, -1, -1) for i in range(2))
+    ref, tol = attention_ref(q, k, v, 0.1, 1, None, dt)
+    last = Tq - 1                                                                   # the row that sees the last key
+    q[0, last - 1, 0, 3], q[1, last, 1, ::2] = math.nan, math.inf
+    kv[0, 0, 1, Tk - 1, 5] = math.nan                                               # seen by the last row of heads 2 and 3
+    bad = torch.zeros(B, Tq, H, dtype=torch.bool, device="cuda")
+    bad[0, last - 1, 0] = bad[1, last, 1] = True
+    bad[:, last, 2:] = True
+    buf = torch.full((B, Tq + 2, H + 1, D), 777.0, dtype=DT[dt][0], device="cuda")
+    out = buf[:, 1:-1, :H]
+    gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, 0.1, 1, None, 0, out)
+    settle()
+    assert bool(torch.isnan(out[bad]).all())
+    check(out[~bad], ref[~bad], tol[~bad], "other rows")
+    assert not out[:, :Tq - Tk].any()                                               # rows without a key
+    out.fill_(777.0)
+    assert bool((buf == 777.0).all())
 
 
 @pytest.mark.parametrize("D", [64, 128])
