@@ -503,9 +503,9 @@ cudaError_t go(const AttentionArgs& a, unsigned work, int S, cudaStream_t stream
 // sectors), a thread has two rows and keeps their scores in registers; K and V, zeros where hidden, lie in
 // shared memory, and a read of 64 bytes of it serves the warp's 16 rows. Two shuffles add up a score.
 // Bound by HBM at a few keys, by those reads from 16 on. Measured (B200, us, keys 3 / 8 / 16 / 24, the
-// tensor-core kernel in brackets): 54 x 131 rows of 20 heads of 64 20.6 / 27.1 / 42.4 / 61.2 (122 to 123),
-// 4 x 1024 rows of 8 heads of 128 7.7 / 9.9 / 18.7 / 24.5 (25), 2304 rows of 16 heads of 64
-// 5.3 / 6.4 / 9.2 / 12.0 (17.6), one row of 16 heads of 128 4.1 / 4.8 / 6.8 / 9.0 (10). At 32 keys it took
+// tensor-core kernel in brackets): 54 x 131 rows of 20 heads of 64 19.0 / 23.5 / 36.3 / 52.0 (122 to 123),
+// 4 x 1024 rows of 8 heads of 128 7.8 / 10.0 / 19 / 24 to 26 (25), 2304 rows of 16 heads of 64
+// 5.3 / 6.4 / 9.2 / 12.0 (17.6), one row of 16 heads of 128 4.2 / 4.8 / 7.0 / 8.7 (10). At 32 keys it took
 // 85 (123), 31 (25), 20 (17.7) and 11.2 (10).
 namespace att32few {
 
@@ -554,6 +554,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
     }
   }
   __syncthreads();
+  if (static_cast<long long>(tile) * kRows + (threadIdx.x >> 5) * 8 >= a.Tq) return;   // a warp without a row
 
   const float scale_log2 = a.scale * 1.4426950408889634f;
   float w[R][KMAX], inv[R];
