@@ -1,6 +1,6 @@
-// gkd_attention for fp32: out = softmax(scale q k^T) v under a key mask. Two kernels: one on
-// the tensor cores, with fp32 accuracy from bf16 products, which this comment describes, and
-// one on the fma units for up to 24 keys, below.
+// gkd_attention for fp32: out = softmax(scale q k^T) v under a key mask. Three kernels: one
+// on the tensor cores, with fp32 accuracy from bf16 products, which this comment describes, and
+// below it two on the fma units, for up to 24 keys and for up to 16 queries.
 //
 // Every operand is taken as x = b0 + b1 + b2, b0 = bf16(x), b1 = bf16(x - b0), b2 =
 // bf16(x - b0 - b1): 24 bits. Of the nine products per term the six with i + j <= 2 are
@@ -646,11 +646,221 @@ cudaError_t go(const AttentionArgs& a, cudaStream_t stream) {
 
 }  // namespace att32few
 
+// Up to 16 queries (decoding, pooled tokens): K and V go from memory straight into registers and the products
+// are fp32 fmas. A CTA has R rows, of all query heads that share a key head (row u is query u / g of head
+// u % g): 4, or 1 for a single query without shared heads. L lanes share a key (16-byte pieces l, l + L, ..),
+// the groups of a CTA stride through the keys, two at a time, and each keeps its own running maximum, sum and
+// output, so that no group waits for another. They are joined at the end: a warp's by shuffles, the warps'
+// and those of a cluster of S CTAs (while the GPU has places left) through shared memory, in a fixed order.
+// With four rows a thread needs 245 registers (two CTAs per SM); held to 168, or one key at a time in 128,
+// it spilled and took twice as long.
+// One row is bound by HBM, four by fmas and issue. Measured (B200, us, 1 / 5 / 16 queries, the tensor-core
+// kernel, which has 128 rows whatever it gets, in brackets): 57 batches of 20 heads of 64 over 4358 keys with
+// holes 222 / 581 / 1112 (1502 to 1506), 64 of 16 heads over 581 55.5 / 111 / 217 (254), one batch over
+// 2304 9.1 / 13.7 / 16.1 (28), 8 of 8 heads of 128 over 581 8.4 / 15.7 / 27.7 (37 to 39), 16 batches of
+// 16 heads on 4 key heads 10.0 / 25.8 / 51 (70). At 32 queries that would be even.
+namespace att32rows {
+
+constexpr int kThreads = 128, kWarps = kThreads / 32, NP = 4, U = 2;
+
+template <int L, int R>                             // lanes per key, NP pieces of 16 bytes each: D <= 16 L; rows
+__global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const __grid_constant__ AttentionArgs a, int S) {
+  constexpr int kGroups = kThreads / L, kRow = L * NP;             // pieces of a row
+  __shared__ float4 qs[R * kRow], part[kWarps * R * kRow];
+  __shared__ float pm[kWarps * R], pl[kWarps * R];
+  const int g = a.q.heads / a.k.heads;
+  const long long rows = static_cast<long long>(a.Tq) * g;
+  const int ntiles = static_cast<int>((rows + R - 1) / R);
+  const int rank = blockIdx.x % S, work = blockIdx.x / S;          // = the rank in the cluster
+  const int tile = work % ntiles, hk = work / ntiles % a.k.heads, b = work / ntiles / a.k.heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, piece = lane % L, group = threadIdx.x / L, nq4 = a.D / 4;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
+  const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+
+  for (int i = threadIdx.x; i < R * kRow; i += kThreads) {
+    const long long u = static_cast<long long>(tile) * R + i / kRow;
+    const int c = i % kRow;
+    qs[i] = u < rows && c < nq4 ? load4(static_cast<const float*>(a.q.data) + b * a.q.batch_stride + u / g * a.q.row_stride +
+                                        (hk * g + u % g) * a.q.head_stride + 4 * c)
+                                : zero;
+  }
+  int see[R], most = 0;                             // keys up to each row's diagonal
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const long long u = static_cast<long long>(tile) * R + r;
+    see[r] = u >= rows    ? 0
+             : a.causal   ? static_cast<int>(max(0ll, min(u / g + a.Tk - a.Tq + 1, static_cast<long long>(a.Tk))))
+                          : a.Tk;
+    most = max(most, see[r]);
+  }
+  const int lo = static_cast<int>(static_cast<long long>(most) * rank / S);
+  const int hi = static_cast<int>(static_cast<long long>(most) * (rank + 1) / S);
+  const int turns = (hi - lo + kGroups * U - 1) / (kGroups * U);   // the same for all: the shuffles want whole warps
+  float m[R], l[R];
+  float4 acc[R][NP];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NP; ++c) acc[r][c] = zero;
+  }
+  uint8_t ahead[U];                                 // mask bytes of the coming keys
+  auto fetch = [&](int n) {
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const long long key = lo + static_cast<long long>(n * U + e) * kGroups + group;
+      ahead[e] = key < hi ? (mask ? mask[key] : 1) : 0;
+    }
+  };
+  fetch(0);
+  __syncthreads();
+  for (int n = 0; n < turns; ++n) {
+    float4 y[U][NP], z[U][NP];
+    bool live[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const long long key = lo + static_cast<long long>(n * U + e) * kGroups + group;
+      live[e] = ahead[e] != 0;                      // hidden keys and values are not read
+#pragma unroll
+      for (int c = 0; c < NP; ++c) y[e][c] = live[e] && L * c + piece < nq4 ? load4(k + key * a.k.row_stride + 4 * (L * c + piece)) : zero;
+#pragma unroll
+      for (int c = 0; c < NP; ++c) z[e][c] = live[e] && L * c + piece < nq4 ? load4(v + key * a.v.row_stride + 4 * (L * c + piece)) : zero;
+    }
+    fetch(n + 1);
+    float s[R][U];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int e = 0; e < U; ++e) s[r][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NP; ++c) {
+        const float4 x = qs[r * kRow + L * c + piece];
+#pragma unroll
+        for (int e = 0; e < U; ++e)
+          s[r][e] = fmaf(x.x, y[e][c].x, fmaf(x.y, y[e][c].y, fmaf(x.z, y[e][c].z, fmaf(x.w, y[e][c].w, s[r][e]))));
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < L; d *= 2)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < U; ++e) s[r][e] += __shfl_xor_sync(0xffffffffu, s[r][e], d);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int e = 0; e < U; ++e)
+        if (!live[e] || lo + (n * U + e) * kGroups + group >= see[r]) s[r][e] = -INFINITY;
+      const float top = max3_nan(m[r], s[r][0], s[r][U - 1]);      // NaN if any score was
+      if (top != m[r]) {
+        const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
+        m[r] = top;
+        l[r] *= f;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+          acc[r][c] = make_float4(acc[r][c].x * f, acc[r][c].y * f, acc[r][c].z * f, acc[r][c].w * f);
+      }
+      const float base = top == -INFINITY ? 0.f : top * scale_log2;          // no key yet: every weight is 0
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        const float p = ex2_approx(fmaf(s[r][e], scale_log2, -base));
+        l[r] += p;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+          acc[r][c] = make_float4(fmaf(p, z[e][c].x, acc[r][c].x), fmaf(p, z[e][c].y, acc[r][c].y),
+                                  fmaf(p, z[e][c].z, acc[r][c].z), fmaf(p, z[e][c].w, acc[r][c].w));
+      }
+    }
+  }
+  // the warp's groups
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float top = m[r];
+#pragma unroll
+    for (int d = L; d <= 16; d *= 2) {
+      const float t = __shfl_xor_sync(0xffffffffu, top, d);
+      top = max3_nan(top, t, t);
+    }
+    const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
+    float sum = l[r] * f;
+#pragma unroll
+    for (int d = L; d <= 16; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+      float4 o = make_float4(acc[r][c].x * f, acc[r][c].y * f, acc[r][c].z * f, acc[r][c].w * f);
+#pragma unroll
+      for (int d = L; d <= 16; d *= 2) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+      }
+      if (lane < L) part[(warp * R + r) * kRow + L * c + piece] = o;
+    }
+    if (lane == 0) {
+      pm[warp * R + r] = top;
+      pl[warp * R + r] = sum;
+    }
+  }
+  __syncthreads();
+  if (S > 1) cluster_sync();
+  const uint32_t om = smem_u32(pm), ol = smem_u32(pl), oo = smem_u32(part);
+  for (int i = threadIdx.x * S + rank; i < R * nq4; i += kThreads * S) {
+    const int r = i / nq4, c = i % nq4;
+    const long long u = static_cast<long long>(tile) * R + r;
+    if (u >= rows) continue;
+    float top = -INFINITY, sum = 0.f;
+    float4 o = zero;
+#pragma unroll 4
+    for (int w = 0; w < S * kWarps; ++w) {          // a NaN among them comes back through its own weight
+      const uint32_t at = om + 4 * (w % kWarps * R + r);
+      top = fmaxf(top, S > 1 ? cluster_load1(cluster_map(at, w / kWarps)) : pm[w * R + r]);
+    }
+#pragma unroll 4
+    for (int w = 0; w < S * kWarps; ++w) {
+      const int own = w % kWarps * R + r;
+      const float mw = S > 1 ? cluster_load1(cluster_map(om + 4 * own, w / kWarps)) : pm[own];
+      const float lw = S > 1 ? cluster_load1(cluster_map(ol + 4 * own, w / kWarps)) : pl[own];
+      const float4 ow = S > 1 ? cluster_load4(cluster_map(oo + 16 * (own * kRow + c), w / kWarps)) : part[own * kRow + c];
+      const float f = mw == -INFINITY ? 0.f : ex2_approx((mw - top) * scale_log2);
+      sum = fmaf(f, lw, sum);
+      o = make_float4(fmaf(f, ow.x, o.x), fmaf(f, ow.y, o.y), fmaf(f, ow.z, o.z), fmaf(f, ow.w, o.w));
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + u / g * a.out.row_stride + (hk * g + u % g) * a.out.head_stride +
+               4 * c,
+           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync();                        // nobody leaves while its shared memory is read
+}
+
+template <int L, int R>
+cudaError_t go(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(a.Tq) * (a.q.heads / a.k.heads);
+  const long long work = (rows + R - 1) / R * a.k.heads * a.B;     // below 2^31: at most 16 x 1024 x 65535 rows
+  int S = 1;                                        // up to two CTAs per SM, at least 128 keys each
+  while (S < 8 && work * S * 2 <= 2 * num_sms && a.Tk >= 256 * S) S *= 2;
+  return launch_cluster(attention_few_rows_kernel<L, R>, dim3(static_cast<unsigned>(work * S)), kThreads, 0, S, stream, a, S);
+}
+
+}  // namespace att32rows
+
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
   // few keys: fma units, above 24 tensor cores (both sides beside that kernel)
   if (a.Tk <= 8) return att32few::go<8>(a, stream);
   if (a.Tk <= 16) return att32few::go<16>(a, stream);
   if (a.Tk <= 24) return att32few::go<24>(a, stream);
+  // few rows, whatever the number of keys: fma units (both sides beside that kernel)
+  if (a.Tq <= 16) {
+    using namespace att32rows;
+    if (a.Tq == 1 && a.q.heads == a.k.heads) return a.D <= 64 ? go<4, 1>(a, num_sms, stream) : go<8, 1>(a, num_sms, stream);
+    return a.D <= 64 ? go<4, 4>(a, num_sms, stream) : go<8, 4>(a, num_sms, stream);
+  }
   using namespace att32;
   const long long work = (static_cast<long long>(a.Tq) + kRows - 1) / kRows * a.q.heads * a.B;
   // few query tiles: a cluster shares the keys of one, while that keeps to one CTA per SM (and to

@@ -378,6 +378,15 @@ ATTENTION += [(2, q, k, 4, hk, D, "f32", causal, kind)
                   (300, 17, 4, 104, 0, "holes"), (5, 24, 1, 128, 1, "prefix"), (129, 24, 4, 64, 0, "all"), (129, 25, 4, 64, 0, "all"),
                   (40, 32, 2, 64, 1, "holes"), (70, 33, 4, 128, 0, "holes")]]
 
+# few rows: one alone, shared heads, both sides of the rule, keys from one turn of a group to several CTAs' shares
+ATTENTION += [(2, q, k, 4, hk, D, "f32", causal, kind)
+              for q, k, hk, D, causal, kind in [
+                  (1, 25, 4, 64, 0, "prefix"), (1, 64, 4, 128, 1, "holes"), (1, 65, 4, 8, 0, "last"), (1, 4613, 4, 64, 0, "holes"),
+                  (1, 5000, 4, 104, 0, "prefix"), (1, 700, 1, 64, 0, "holes"), (2, 255, 4, 64, 1, "all"), (3, 256, 2, 72, 0, "holes"),
+                  (5, 4358, 4, 64, 0, "holes"), (7, 2049, 1, 128, 1, "prefix"), (16, 300, 4, 64, 1, "holes"), (16, 1111, 4, 96, 0, "all"),
+                  (17, 300, 4, 64, 1, "holes")]]
+ATTENTION += [(300, 5, 333, 4, 2, 64, "f32", 1, "holes"), (300, 1, 333, 4, 4, 128, "f32", 0, "holes")]
+
 
 @pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "-".join(str(v) for v in c))
 def test_attention(case):
@@ -447,14 +456,15 @@ def test_attention_keys_past_32_bit_offsets(dt):
     check(out, *attention_ref(q, rows[None, :, None], v, 0.5, 0, None, dt), "far keys")
 
 
-def test_attention_many_keys_past_32_bit_offsets():
+@pytest.mark.parametrize("Tq", [1, 3, 40])
+def test_attention_many_keys_past_32_bit_offsets(Tq):
     Tk, D, stride = 30, 64, 2 ** 27 + 64
     buf = torch.empty((Tk - 1) * stride + D, device="cuda")
     rows, k = rand(1, Tk, D, dt="f32"), rand(2, 1, Tk, 1, D, dt="f32")
     v = buf.as_strided((1, Tk, 1, D), (0, stride, D, 1))
     v[0, :, 0] = rows
-    q, out = rand(3, 1, 3, 1, D, dt="f32", std=3.0), torch.empty(1, 3, 1, D, device="cuda")
-    gk.gkd_attention(q, k, v, DT["f32"][1], 1, 3, Tk, D, 0.5, 0, None, 0, out)
+    q, out = rand(3, 1, Tq, 1, D, dt="f32", std=3.0), torch.empty(1, Tq, 1, D, device="cuda")
+    gk.gkd_attention(q, k, v, DT["f32"][1], 1, Tq, Tk, D, 0.5, 0, None, 0, out)
     settle()
     check(out, *attention_ref(q, k, rows[None, :, None], 0.5, 0, None, "f32"), "far values")
 
@@ -482,6 +492,28 @@ def test_attention_over_few_keys_on_slices_with_nan(dt, Tk):
     assert bool(torch.isnan(out[bad]).all())
     check(out[~bad], ref[~bad], tol[~bad], "other rows")
     assert not out[:, :Tq - Tk].any()                                               # rows without a key
+    out.fill_(777.0)
+    assert bool((buf == 777.0).all())
+
+
+@pytest.mark.parametrize("Tq,Hk", [(1, 4), (1, 2), (6, 2), (16, 4)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attention_of_few_rows_on_slices_with_nan(dt, Tq, Hk):
+    B, Tk, H, D = 3, 1500, 4, 64
+    q = rand(1, B, Tq + 3, H + 2, D + 16, dt=dt)[:, 2:Tq + 2, 1:H + 1, 8:D + 8]
+    k, v = (rand(i, 1, Hk, Tk, D, dt=dt).transpose(1, 2).expand(B, -1, -1, -1) for i in (2, 3))
+    ref, tol = attention_ref(q, k, v, 0.1, 1, None, dt)
+    bad = torch.zeros(B, Tq, H, dtype=torch.bool, device="cuda")
+    q[0, 0, 0, 3], q[1, Tq - 1, 1, ::2] = math.nan, math.inf
+    bad[0, 0, 0] = bad[1, Tq - 1, 1] = True
+    k[0, Tk - 1, Hk - 1, 5] = math.nan                                              # seen by the last row of the last heads
+    bad[:, Tq - 1, H - H // Hk:] = True
+    buf = torch.full((B, Tq + 2, H + 1, D), 777.0, dtype=DT[dt][0], device="cuda")
+    out = buf[:, 1:-1, :H]
+    gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, 0.1, 1, None, 0, out)
+    settle()
+    assert bool(torch.isnan(out[bad]).all())
+    check(out[~bad], ref[~bad], tol[~bad], "other rows")
     out.fill_(777.0)
     assert bool((buf == 777.0).all())
 
