@@ -137,8 +137,9 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  * dt = GKD_BF16: tensor-core products with fp32 accumulation; maxima, sums and
  * exponentials in fp32; the weights p_j are rounded to bf16 for the product with v
  * (their sum is not). dt = GKD_F32: every operand as three bf16 numbers (24 bits), six
- * products per term, the rest in fp32 (up to 24 keys or 16 queries: fp32 fused multiply-adds); visible
- * values must be finite and below 2^127 in magnitude (others can give NaN). A row with a NaN or infinite score is NaN.
+ * products per term, the rest in fp32 (up to 24 keys or 16 queries: fp32 fused
+ * multiply-adds); visible values must be finite and below 2^127 in magnitude (others can
+ * give NaN). A row with a NaN or infinite score is NaN.
  * Limits: 0 <= B <= 65535, 0 <= Tq, Tk < 2^31 - 256, 8 <= D <= 128, D % 8 == 0,
  * 1 <= heads <= 1024, scale finite and positive.
  */
