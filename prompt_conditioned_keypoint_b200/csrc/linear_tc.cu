@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
   RowsCtl* ctl = reinterpret_cast<RowsCtl*>(bufs + kEpiWarps * 2 * kBufBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ncol = (a.Cout + NT - 1) / NT;
-  const long long ntiles = static_cast<long long>((a.T + kM - 1) / kM) * ncol;
+  const long long ntiles = (static_cast<long long>(a.T) + kM - 1) / kM * ncol;
   const int nk = (a.Cin + kChunk - 1) / kChunk;
   const int flush = F32OUT ? kFlush : nk;            // stages per accumulator
   const uint64_t lim = a.wait_limit_ns;
