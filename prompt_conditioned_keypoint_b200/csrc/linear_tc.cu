@@ -17,10 +17,10 @@
 // 1024 58 us = 1334 TFLOP/s, 73 with scale and residual onto fp32; 17 x 1280 -> 2048 6.1 us.
 //
 // The tensor core truncates each K = 16 step's sum, so a sum of Cin products
-// drifts towards zero by about Cin / 32 of 2^-23 (measured: 1.0e-6 of the result
-// at 1024 channels, 4.4e-6 at 4096, against 6e-7 for fp32 fused multiply-adds).
-// A bf16 output does not see that; for an fp32 output sums of at most 512
-// channels stay in the accumulator and are added up by the epilogue in fp32.
+// drifts towards zero (sums of positive products: 3.7e-7 of the result at 512 channels,
+// 1.1e-6 at 1024, 3.4e-6 at 2048). A bf16 output does not see that; for an fp32 output
+// sums of at most 512 channels stay in an accumulator and are added up in fp32 by the
+// epilogue's warps, in both kernels and for every Cin.
 #include "blocks_common.cuh"
 #include "gkd_internal.h"
 
@@ -342,13 +342,14 @@ struct SplitArgs {
   void* out;
   long long residual_stride, out_stride;
   int T, Cin, Cout, act;
-  int nparts;                // accumulators side by side (fp32 outputs: at most 512 channels each, where they fit)
   unsigned* err;
   unsigned long long wait_limit_ns;
 };
 
+constexpr int kAccs = 4;                           // accumulators in turn for fp32 outputs (256 columns at N = 64: two CTAs fit)
+
 struct SplitCtl {
-  uint64_t full[6], empty[6], accfull, drain;
+  uint64_t full[6], empty[6], accfull[kAccs], accempty[kAccs], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -371,9 +372,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
   const int nkall = (a.Cin + kChunk - 1) / kChunk;
   const int kb = static_cast<int>(static_cast<long long>(nkall) * rank / S);
   const int nk = static_cast<int>(static_cast<long long>(nkall) * (rank + 1) / S) - kb;   // may be 0
-  const int per = max(1, (nk + a.nparts - 1) / a.nparts);            // stages per accumulator
-  const int parts = (nk + per - 1) / per;
-  const uint32_t ncols = a.nparts * N < 32 ? 32u : static_cast<uint32_t>(a.nparts * N);   // nparts: a power of 2
+  constexpr bool kTurns = sizeof(TO) == 4;           // accumulators of kFlush stages in turn, else one for all
+  const int parts = kTurns ? (nk + kFlush - 1) / kFlush : min(nk, 1);
+  constexpr uint32_t ncols = kTurns ? kAccs * N : N < 32 ? 32 : N;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abortp = &ctl->abort_flag;
 
@@ -382,7 +383,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    mbar_init(&ctl->accfull, 1);
+    for (int s = 0; s < kAccs; ++s) {
+      mbar_init(&ctl->accfull[s], 1);
+      mbar_init(&ctl->accempty[s], 4);
+    }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -420,17 +424,24 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     const uint64_t wdesc = umma_desc_sw128(smem_u32(smem)), xdesc = umma_desc_sw128(smem_u32(smem) + kWBytes);
     bool ok = true;
     uint32_t it = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw) && ok;
+      return ok;
+    };
     for (; it < static_cast<uint32_t>(nk); ++it) {
       const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
-      const bool okw = mbar_wait_bounded(&ctl->full[s], ph, lim, abortp);
-      ok = __all_sync(0xffffffffu, okw);
-      if (!ok) break;
+      const uint32_t acc = kTurns ? it / kFlush % kAccs : 0, turn = kTurns ? it / (kFlush * kAccs) : 0;
+      const bool fresh = kTurns ? it % kFlush == 0 : it == 0;
+      if (fresh && turn > 0 && !wait(&ctl->accempty[acc], (turn & 1) ^ 1)) break;
+      if (!wait(&ctl->full[s], ph)) break;
       tc_fence_after();
       const uint64_t off = static_cast<uint64_t>((s * kBytes) >> 4);
-      umma_ss_f16_x4_elect(tmem + (it / per) * N, wdesc + off, xdesc + off, idesc, it % per ? 1u : 0u);
+      umma_ss_f16_x4_elect(tmem + acc * N, wdesc + off, xdesc + off, idesc, fresh ? 0u : 1u);
       umma_commit_elect(&ctl->empty[s]);
+      if ((kTurns && it % kFlush == kFlush - 1) || it + 1 == static_cast<uint32_t>(nk))
+        umma_commit_elect(&ctl->accfull[acc]);
     }
-    if (ok) umma_commit_elect(&ctl->accfull);
     if (!ok && lane == 0) {
       ctl->abort_flag = 1;
       atomicOr(a.err, kErrTimeout);
@@ -445,25 +456,32 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
   float* part = reinterpret_cast<float*>(smem);
   if (warp >= 4) {
     const int q = warp & 3;
-    const bool okw = mbar_wait_bounded(&ctl->accfull, 0, lim, abortp);
-    if (__all_sync(0xffffffffu, okw)) {
+    const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = 0.f;
+    bool ok = true;
+    for (int p = 0; p < parts; ++p) {
+      const int acc = p % kAccs;
+      const bool okw = mbar_wait_bounded(&ctl->accfull[acc], (p / kAccs) & 1, lim, abortp);
+      ok = __all_sync(0xffffffffu, okw);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
       for (int g = 0; g < N / 16; ++g) {
-        float v[16];
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(src + acc * N + 16 * g, r);
+        tmem_wait_ld_regs(r);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = 0.f;
-        for (int p = 0; p < parts; ++p) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(src + p * N + 16 * g, r);
-          tmem_wait_ld_regs(r);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) part[(16 * g + j) * 128 + 32 * q + lane] = v[j];
+        for (int j = 0; j < 16; ++j) v[16 * g + j] += __uint_as_float(r[j]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->accempty[acc]);
+    }
+    if (ok) {                                          // the last products have ended: nothing reads the ring any more
+#pragma unroll
+      for (int j = 0; j < N; ++j) part[j * 128 + 32 * q + lane] = v[j];
     } else if (lane == 0) {
       ctl->abort_flag = 1;
       atomicOr(a.err, kErrTimeout);
@@ -582,10 +600,6 @@ cudaError_t launch_split(const LinearArgs& a, int S, cudaStream_t stream, const 
   p.act = a.act;
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
-  p.nparts = 1;
-  const int per_cta = ((a.Cin + kChunk - 1) / kChunk + S - 1) / S;
-  if (!a.out_bf16)
-    while (p.nparts * kFlush < per_cta && 2 * p.nparts * N <= 512) p.nparts *= 2;
   const unsigned ctiles = (a.Cout + 127) / 128, rtiles = (static_cast<unsigned>(a.T) + N - 1) / N;
   return a.out_bf16 ? go_split<N, __nv_bfloat16>(p, S, ctiles, rtiles, stream)
                     : go_split<N, float>(p, S, ctiles, rtiles, stream);
@@ -623,14 +637,10 @@ cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stre
   // with 1, 2, 4, 8; 80 x 1024 -> 1024: 9.8, 8.5, 7.3, 7.8 us; 256 x 1024 -> 1024, where 8 would
   // be two CTAs per SM: 7.8 us with 4, 9.8 with 8; one tile of 128 columns instead: 10.1 us).
   const int nk = (a.Cin + kChunk - 1) / kChunk;
-  int N = a.T <= 32 ? 16 : a.T <= 64 ? 32 : 64, S;
-  for (;; N /= 2) {
-    const long long tiles = (static_cast<long long>(a.T) + N - 1) / N * ctiles(128);
-    S = 1;
-    while (S < 8 && tiles * 2 * S <= num_sms + num_sms / 8 && nk >= (tiles * 4 * S <= num_sms ? 4 : 8) * S) S *= 2;
-    // an fp32 output wants at most 512 channels per accumulator: narrower tiles leave room for more of them
-    if (a.out_bf16 || N == 16 || (nk + S - 1) / S <= 512 / N * kFlush) break;
-  }
+  const int N = a.T <= 32 ? 16 : a.T <= 64 ? 32 : 64;
+  const long long tiles = (static_cast<long long>(a.T) + N - 1) / N * ctiles(128);
+  int S = 1;
+  while (S < 8 && tiles * 2 * S <= num_sms + num_sms / 8 && nk >= (tiles * 4 * S <= num_sms ? 4 : 8) * S) S *= 2;
   switch (N) {
     case 16:
       return launch_split<16>(a, S, stream, why);
