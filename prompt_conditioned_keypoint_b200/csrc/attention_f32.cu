@@ -52,6 +52,7 @@ struct Plan {
     uint64_t qready, kready[kStages], kempty[kStages], vready[kStages], vempty[kStages];
     uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], odone[2], drain;
     Info info[kInfo];
+    int first;                                      // the first key that the mask leaves in this CTA's tiles
     uint32_t tmem_base;
     int abort_flag;
     float m[kRows], l[kRows];                       // of the rows, for the other CTAs of the cluster
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
           f.k0 = end ? -1 : t * BN;
           f.plain = every == 0xffffffffu && t < seen;
           f.words = bits[1] ? 2 : 1;
+          if (n == 0 && !end) ctl->first = t * BN + (bits[0] ? __ffs(bits[0]) : 32 + __ffs(bits[1])) - 1;
           f.bits[0] = bits[0];
           f.bits[1] = bits[1];
           mbar_arrive(&ctl->ifull[is]);
@@ -357,8 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     if (ok && j > 0 && active) gather(j - 1, 1.f);
     if (S > 1 && j == 0) wait(&ctl->qready, 0);     // no tile: Q's planes, which the share overwrites, may still be written
     if (!ok) give_up();
+    // No score above -inf: a row that sees a key all the same is 0 / 0, one without a key is 0. Their sums are
+    // both 0 so far; 1 marks the first.
+    if (ok && j > 0 && m == -INFINITY && (!a.causal || ctl->first <= r0 + r + shift)) l = 1.f;
     if (S == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
       float* o = static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride;
       if (ok && r0 + r < a.Tq) {
 #pragma unroll
@@ -478,7 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (top == -INFINITY)                         // no score above -inf in any share: their marks
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) l += cluster_load1(cluster_map(ol + 4 * r, s));
+      const float inv = l == 0.f ? 0.f : top == -INFINITY ? NAN : 1.f / l;
       store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride + 4 * c,
              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
@@ -603,7 +611,8 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
       sum[j & 3] += w[i][j];
     }
     const float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    inv[i] = l == 0.f ? 0.f : 1.f / l;
+    // no score above -inf: 0 / 0 for a row that sees a key, 0 for one without
+    inv[i] = top == -INFINITY ? (bits ? NAN : 0.f) : 1.f / l;
   }
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
@@ -776,6 +785,17 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       }
     }
   }
+  // A row without a score above -inf may see a key all the same: the first one that the mask leaves in the group.
+  // (Noted in the loop it took 2% of 5 and 16 rows' time.)
+  int first = 0x7fffffff;
+  bool low = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) low |= m[r] == -INFINITY;
+  if (low) {
+#pragma unroll 1
+    for (int key = lo + group; key < hi && first > key; key += kGroups)
+      if (!mask || mask[key]) first = key;
+  }
   // the warp's groups
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -786,7 +806,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       top = max3_nan(top, t, t);
     }
     const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
-    float sum = l[r] * f;
+    // no score above -inf in the warp: 1 marks that the row sees a key all the same
+    float sum = top == -INFINITY ? (first < see[r] ? 1.f : 0.f) : l[r] * f;
 #pragma unroll
     for (int d = L; d <= 16; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
 #pragma unroll
@@ -830,7 +851,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       sum = fmaf(f, lw, sum);
       o = make_float4(fmaf(f, ow.x, o.x), fmaf(f, ow.y, o.y), fmaf(f, ow.z, o.z), fmaf(f, ow.w, o.w));
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (top == -INFINITY)                           // none in any warp: 0 / 0 for a row that sees a key, 0 for one without
+#pragma unroll 1
+      for (int w = 0; w < S * kWarps; ++w) {
+        const int own = w % kWarps * R + r;
+        sum += S > 1 ? cluster_load1(cluster_map(ol + 4 * own, w / kWarps)) : pl[own];
+      }
+    const float inv = sum == 0.f ? 0.f : top == -INFINITY ? NAN : 1.f / sum;
     store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + u / g * a.out.row_stride + (hk * g + u % g) * a.out.head_stride +
                4 * c,
            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));

@@ -73,6 +73,7 @@ struct Ctl {
   uint64_t qfull, kfull[kKvStages], kempty[kKvStages], vfull[kKvStages], vempty[kKvStages];
   uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], pvdone, odone, drain;
   Info info[kInfo];
+  int first;                                        // the first key that the mask leaves in this CTA's tiles
   uint32_t tmem_base;
   int abort_flag;
   float m[kRows], l[kRows];                         // of the rows, for the other CTAs of the cluster
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     mbar_init(&ctl->odone, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
+    ctl->first = lo * BN;                           // with a mask set anew
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
           Info& f = ctl->info[is];
           f.k0 = end ? -1 : k0;
           if (!end) {
+            if (n == 0) ctl->first = k0 + (bits[0] ? __ffs(bits[0]) : 32 + __ffs(bits[W - 1])) - 1;
             f.plain = every == 0xffffffffu && t < seen;
             f.words = 1;
 #pragma unroll
@@ -471,7 +474,10 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     }
     if (!ok && lane == 0) give_up();
     const bool mine = ok && r0 + r < a.Tq;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // No score above -inf: a row that sees a key all the same is 0 / 0, one without a key is 0. Their sums are
+    // both 0 so far; 1 marks the first.
+    if (ok && j > 0 && m == -INFINITY && (!a.causal || ctl->first <= r0 + r + static_cast<long long>(a.Tk) - a.Tq)) l = 1.f;
+    const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs;
     if (S > 1) {
       ctl->m[r] = m;
@@ -536,7 +542,10 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (m == -INFINITY)                           // no score above -inf in any share: their marks
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) l += cluster_load1(cluster_map(ol + 4 * r, s));
+      const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
       store4(static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs + 4 * c,
              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }

@@ -1,10 +1,12 @@
 """GPU: the transformer-block operators at the ends of what their header allows: the longest row count, infinite and
 very large scores, long sums, waits that run out."""
+import math
+
 import pytest
 import torch
 
 from prompt_conditioned_keypoint_b200 import binding as gk
-from test_gpu_blocks import check, linear_ref, rand, settle
+from test_gpu_blocks import DT, check, linear_ref, rand, settle, unit
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,61 @@ def test_linear_fp32_output_of_long_sums_does_not_drift(T, Cin, Cout):
     assert abs(off.mean().item()) <= 2.0 ** -20
     # every step of an accumulator (32 of them) and every addition off by a whole unit of the sum so far, which averages half
     assert off.abs().max().item() <= (16.5 + Cin / 512 / 4) * 2.0 ** -23
+
+
+# ------------------------------------------------------------------ infinite scores
+# Every attention kernel: fp32 by its rules for keys and rows, bf16 by the width of a head; with one CTA per query tile
+# and with clusters that share the keys.
+KERNELS = [
+    # B, Tq, Tk, H, Hk, D, dt
+    (3, 40, 3, 2, 2, 64, "f32"), (3, 70, 24, 2, 1, 128, "f32"),
+    (3, 1, 40, 2, 2, 64, "f32"), (3, 1, 1500, 2, 2, 128, "f32"), (3, 5, 300, 4, 2, 64, "f32"), (3, 16, 900, 2, 1, 128, "f32"),
+    (3, 40, 100, 2, 2, 64, "f32"), (3, 200, 700, 2, 1, 64, "f32"), (3, 150, 1000, 2, 2, 128, "f32"), (90, 130, 90, 2, 2, 72, "f32"),
+    (3, 1, 40, 2, 2, 64, "bf16"), (3, 40, 100, 2, 1, 64, "bf16"), (3, 150, 1000, 2, 2, 64, "bf16"), (3, 17, 1500, 2, 2, 128, "bf16"),
+    (90, 130, 90, 4, 2, 80, "bf16"), (90, 260, 130, 4, 2, 64, "bf16"),
+]
+
+
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("case", KERNELS, ids=lambda c: "-".join(str(v) for v in c))
+def test_attention_where_scores_are_minus_infinity(case, causal):
+    """A visible key whose score is -inf has no weight beside others; a row that sees only such keys is NaN (0 / 0 by the
+    definition), not 0 as a row without a key."""
+    B, Tq, Tk, H, Hk, D, dt = case
+    q, k, v = rand(1, B, Tq, H, D, dt=dt), rand(2, B, Tk, Hk, D, dt=dt), rand(3, B, Tk, Hk, D, dt=dt)
+    mask = (torch.rand(B, Tk, generator=torch.Generator().manual_seed(4)) < 0.7).to(torch.uint8).cuda()
+    low = torch.zeros(Tk, dtype=torch.bool, device="cuda")
+    low[:max(1, Tk // 3)] = True                            # these keys' scores overflow for every other row
+    low[Tk // 2] = True
+    mask[:, Tk // 2] = mask[:, Tk - 1] = 1
+    mask[1] = low.to(torch.uint8)                           # a batch that sees nothing else
+    mask[2] = 0                                             # and one that sees no key
+    q[..., 0] = 0
+    q[:, ::2, :, 0] = 2.0 ** 100                            # the product with -2^100 is -inf, with 0 it is 0
+    k[..., 0] = torch.where(low, -2.0 ** 100, 0.0)[None, :, None].to(k.dtype)
+    out = torch.full_like(q, 777.0)
+    gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, D ** -0.5, causal, mask, Tk, out)
+    settle()
+
+    qs, ks = q.double(), k.double().repeat_interleave(H // Hk, 2)
+    big = qs[..., 0] > 0                                    # [B][Tq][H]
+    qs, ks = qs.clone(), ks.clone()
+    qs[..., 0] = 0
+    s = torch.einsum("bihd,bjhd->bhij", qs, ks) * D ** -0.5
+    seen = (mask != 0)[:, None, None].expand(B, H, Tq, Tk)
+    if causal:
+        seen = seen & (torch.arange(Tk, device="cuda")[None] <= torch.arange(Tq, device="cuda")[:, None] + (Tk - Tq))
+    finite = seen & ~(big.permute(0, 2, 1)[..., None] & low)
+    p = torch.nan_to_num(torch.softmax(s.masked_fill(~finite, -math.inf), -1), nan=0.0)
+    vs = v.double().repeat_interleave(H // Hk, 2)
+    ref = torch.einsum("bhij,bjhd->bihd", p, vs)
+    size = torch.einsum("bhij,bjhd->bihd", p, vs.abs())
+    d = (D + 8) * 2.0 ** -23 * D ** -0.5 * torch.einsum("bihd,bjhd->bhij", qs.abs(), ks.abs()).amax(-1).permute(0, 2, 1)
+    tol = unit(dt) * ref.abs() + ((unit(dt) if dt == "bf16" else 0) + 2 * d[..., None] + (Tk + 24) * 2.0 ** -22) * size
+    none, nan = ~seen.any(-1), seen.any(-1) & ~finite.any(-1)
+    none, nan = none.permute(0, 2, 1), nan.permute(0, 2, 1)
+    assert bool(nan.any()) and bool(none.any())
+    assert bool(torch.isnan(out[nan]).all()), "rows whose scores are all -inf"
+    assert not out[none].any(), "rows without a key"
+    rest = ~(nan | none)
+    check(out[rest], ref[rest], tol[rest], "other rows")
