@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
   const int r0 = tile * kRows;
   const long long shift = static_cast<long long>(a.Tk) - a.Tq;     // causal: key j for row i iff j <= i + shift
   const float scale_log2 = a.scale * 1.4426950408889634f;
+  const ScoreScale ss = score_scale(scale_log2);
   const int dk = (a.D + 15) / 16;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abortp = &ctl->abort_flag;
@@ -315,13 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < BN; e += 2) t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], x[e], x[e + 1]);
       const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], m);   // NaN if any score was
-      const float base = top == -INFINITY ? 0.f : top * scale_log2;          // no key yet: every weight is 0
+      const float factor = ss.factor(top), base = ss.offset(top);
       const float f = m == -INFINITY ? 0.f : ex2_approx((m - top) * scale_log2);
       m = top;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < BN; ++e) {
-        x[e] = ex2_approx(fmaf(x[e], scale_log2, -base));
+        x[e] = ex2_approx(fmaf(x[e], factor, -base));
         sum[e & 3] += x[e];
       }
       l = fmaf(l, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
   __syncthreads();
   if (static_cast<long long>(tile) * kRows + (threadIdx.x >> 5) * 8 >= a.Tq) return;   // a warp without a row
 
-  const float scale_log2 = a.scale * 1.4426950408889634f;
+  const ScoreScale ss = score_scale(a.scale * 1.4426950408889634f);
   float w[R][KMAX], inv[R];
 #pragma unroll
   for (int j0 = 0; j0 < KMAX; j0 += 4) {            // four keys at a time: their sums in flight together
@@ -603,11 +604,11 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
       w[i][j + 1] = (bits >> (j + 1)) & 1u ? w[i][j + 1] : -INFINITY;
       top = max3_nan(top, w[i][j], w[i][j + 1]);    // NaN if any score was
     }
-    const float base = top == -INFINITY ? 0.f : top * scale_log2;   // no key: every weight is 0
+    const float factor = ss.factor(top), base = ss.offset(top);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      w[i][j] = ex2_approx(fmaf(w[i][j], scale_log2, -base));
+      w[i][j] = ex2_approx(fmaf(w[i][j], factor, -base));
       sum[j & 3] += w[i][j];
     }
     const float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -688,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
   const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
   const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
   const float scale_log2 = a.scale * 1.4426950408889634f;
+  const ScoreScale ss = score_scale(scale_log2);
 
   for (int i = threadIdx.x; i < R * kRow; i += kThreads) {
     const long long u = static_cast<long long>(tile) * R + i / kRow;
@@ -708,12 +710,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
   const int lo = static_cast<int>(static_cast<long long>(most) * rank / S);
   const int hi = static_cast<int>(static_cast<long long>(most) * (rank + 1) / S);
   const int turns = (hi - lo + kGroups * U - 1) / (kGroups * U);   // the same for all: the shuffles want whole warps
-  float m[R], l[R];
+  float m[R], l[R], base[R];                        // base: of the weights, formed where the maximum changes
   float4 acc[R][NP];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
-    l[r] = 0.f;
+    l[r] = base[r] = 0.f;
 #pragma unroll
     for (int c = 0; c < NP; ++c) acc[r][c] = zero;
   }
@@ -768,15 +770,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       if (top != m[r]) {
         const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
         m[r] = top;
+        base[r] = ss.offset(top);
         l[r] *= f;
 #pragma unroll
         for (int c = 0; c < NP; ++c)
           acc[r][c] = make_float4(acc[r][c].x * f, acc[r][c].y * f, acc[r][c].z * f, acc[r][c].w * f);
       }
-      const float base = top == -INFINITY ? 0.f : top * scale_log2;          // no key yet: every weight is 0
+      const float factor = ss.factor(top);
 #pragma unroll
       for (int e = 0; e < U; ++e) {
-        const float p = ex2_approx(fmaf(s[r][e], scale_log2, -base));
+        const float p = ex2_approx(fmaf(s[r][e], factor, -base[r]));
         l[r] += p;
 #pragma unroll
         for (int c = 0; c < NP; ++c)

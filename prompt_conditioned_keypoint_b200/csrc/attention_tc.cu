@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
-        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), base2 = make_float2(-base, -base);
+        const ScoreScale ss = score_scale(a.scale_log2);
+        const float factor = ss.factor(m), base = ss.offset(m);
+        const float2 scale2 = make_float2(factor, factor), base2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         if (!kHold) load(0);
 #pragma unroll

@@ -103,3 +103,31 @@ def test_attention_where_scores_are_minus_infinity(case, causal):
     assert not out[none].any(), "rows without a key"
     rest = ~(nan | none)
     check(out[rest], ref[rest], tol[rest], "other rows")
+
+
+@pytest.mark.parametrize("case", KERNELS, ids=lambda c: "-".join(str(v) for v in c))
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_scores_beyond_32_bits(case, sign):
+    """Finite scores of some 2^37 of either sign: neighbours are thousands apart, so that a row is its best key's value
+    (the mean of two, where the key stands twice)."""
+    B, Tq, Tk, H, Hk, D, dt = case
+    q, k, v = (rand(i, *s, dt=dt) for i, s in ((1, (B, Tq, H, D)), (2, (B, Tk, Hk, D)), (3, (B, Tk, Hk, D))))
+    q, k = q * 2.0 ** 17, k * 2.0 ** 17
+    if sign < 0:                                            # the best of a row is far below 0
+        q, k = q.abs(), -k.abs()
+    k[:, Tk - 1] = k[:, 0]
+    out = torch.full_like(q, 777.0)
+    gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, 1.0, 0, None, 0, out)
+    settle()
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), k.double().repeat_interleave(H // Hk, 2))
+    vs = v.double().repeat_interleave(H // Hk, 2)
+    # the keys 0 and Tk - 1 count as one
+    best, at = s[..., :-1].topk(2 if Tk > 2 else 1, -1)
+    slack = (D + 8) * 2.0 ** -23 * torch.einsum("bihd,bjhd->bhij", q.double().abs(), k.double().abs().repeat_interleave(H // Hk, 2)).amax(-1)
+    clear = best[..., 0] - best[..., 1] > 2 * slack + 200   # rounding does not change the order, and 2^-288 is nothing
+    assert clear.double().mean().item() > 0.9
+    win = at[..., 0].permute(0, 2, 1)                       # [B][Tq][H]
+    ref = torch.gather(vs, 1, win[..., None].expand(B, Tq, H, D))
+    ref = torch.where((win == 0)[..., None], (ref + vs[:, Tk - 1:Tk]) / 2, ref)
+    clear = clear.permute(0, 2, 1)
+    check(out[clear], ref[clear], (unit(dt) * ref.abs() + 2.0 ** -22 * (vs.abs().amax(1, keepdim=True)))[clear], "best key's value")
