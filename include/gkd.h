@@ -51,7 +51,8 @@
  *     once. gkd_last_error() is per thread. The wait limit
  *     (gkd_set_wait_timeout_ms) and the debug flags (gkd_debug_set_flags) are
  *     process-wide: the flags are consumed by whichever bf16 gkd_heatmap
- *     launch comes next, from any thread.
+ *     (or, in gkd_blocks.h, gkd_linear or gkd_attention) launch comes next,
+ *     from any thread.
  */
 #ifndef GKD_H_
 #define GKD_H_
@@ -355,16 +356,17 @@ GKD_API gkd_status gkd_check_device_error(void* stream);
 
 /*
  * Upper bound, in milliseconds, on any single internal wait of the tensor-core
- * heatmap kernel (default 2000). Process-wide; applies to later launches.
+ * kernels (default 2000). Process-wide; applies to later launches.
  * Returns GKD_ERR_ARG for 0.
  */
 GKD_API gkd_status gkd_set_wait_timeout_ms(unsigned int ms);
 
 /*
- * Test hook: bit 0 makes the next gkd_heatmap launch on the bf16 path withhold
- * its upsample producers' first hand-off to the MMA warp, so the MMA warp's
- * bounded wait runs out and the kernel takes its timeout exit. The flags are
- * consumed (reset to 0) by that launch. Returns GKD_ERR_ARG for unknown bits.
+ * Test hook: bit 0 makes the next gkd_heatmap launch on the bf16 path, or the next
+ * gkd_linear or gkd_attention launch (gkd_blocks.h), withhold its producers' first
+ * hand-off to the MMA warp, so the MMA warp's bounded wait runs out and the kernel
+ * takes its timeout exit. The flags are consumed (reset to 0) by that launch, also
+ * by one of a kernel without such a hand-off. Returns GKD_ERR_ARG for unknown bits.
  */
 GKD_API gkd_status gkd_debug_set_flags(unsigned int flags);
 

@@ -615,6 +615,7 @@ gkd_status gkd_linear(const void* x, gkd_dtype dt, int T, int Cin, long long x_s
   a.out_bf16 = out_dt == GKD_BF16;
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
+  a.withhold = (g_debug_flags.exchange(0) & gkd::kDbgSkipProducerArrive) != 0;
   const char* why = "";
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dt == GKD_BF16 ? gkd::launch_linear_tc(a, ds->num_sms, st, &why)
@@ -756,6 +757,7 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   a.mask_batch_stride = key_mask_batch_stride;
   a.err = ds->err_word;
   a.wait_limit_ns = static_cast<unsigned long long>(g_wait_timeout_ms.load()) * 1000000ull;
+  a.withhold = (g_debug_flags.exchange(0) & gkd::kDbgSkipProducerArrive) != 0;
   const char* why = "";
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = Tk == 0          ? gkd::launch_attention_none(a, size, st)

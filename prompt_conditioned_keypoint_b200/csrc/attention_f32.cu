@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       for (int i = 0; i < BN / kStep; ++i) put(ks, P::kPlane, BN * 128, t / kRow4 + i * kStep, kr[i]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->kready[s]);
+      if (lane == 0 && !(a.withhold && j == 0)) mbar_arrive(&ctl->kready[s]);
       if (j >= kStages && !wait(&ctl->vempty[s], ph ^ 1)) break;
 #pragma unroll
       for (int i = 0; i < BN / kStep; ++i) put(ks + P::kKvBytes, P::kPlane, BN * 128, t / kRow4 + i * kStep, vr[i]);

@@ -60,6 +60,7 @@ struct Args {
   long long mask_bs;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;
 };
 
 struct Info {                                       // one key tile
@@ -216,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
         }
         const uint32_t s = n % kKvStages, ph = (n / kKvStages) & 1;
         if (n < kKvStages || mbar_wait_bounded(&ctl->kempty[s], ph ^ 1, lim, abortp)) {
-          mbar_arrive_expect_tx(&ctl->kfull[s], kKvBytes);
-          for (int c = 0; c < DCH; ++c)
+          if (!(a.withhold && n == 0)) mbar_arrive_expect_tx(&ctl->kfull[s], kKvBytes);
+          for (int c = 0; c < DCH && !(a.withhold && n == 0); ++c)
             tma_load_4d(ks + s * kKvBytes + c * BN * 128, &a.k, &ctl->kfull[s], 64 * c, k0, hk, bk);
           if (n < kKvStages || mbar_wait_bounded(&ctl->vempty[s], ph ^ 1, lim, abortp)) {
             mbar_arrive_expect_tx(&ctl->vfull[s], kKvBytes);
@@ -620,6 +621,7 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_
   p.mask_bs = a.mask_batch_stride;
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
+  p.withhold = a.withhold;
   const long long work = static_cast<long long>(p.ntiles) * a.q.heads * a.B;
   const int ktiles = static_cast<int>((static_cast<long long>(a.Tk) + BN - 1) / BN);
   int S = 1;

@@ -159,6 +159,7 @@ struct LinearArgs {
   bool out_bf16;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;             // test hook: the first stage of every CTA is not handed to the products
 };
 cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16 operands
@@ -197,6 +198,7 @@ struct AttentionArgs {
   long long mask_batch_stride;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;             // test hook: the first tile of keys of every CTA is not handed to the products
 };
 cudaError_t launch_attention_none(const AttentionArgs& a, int size, cudaStream_t stream);   // Tk = 0: zeros
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream);

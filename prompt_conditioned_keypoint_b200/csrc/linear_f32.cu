@@ -49,6 +49,7 @@ struct Args {
   int T, Cin, Cout, act;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;
 };
 
 struct Ctl {
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_f32_kernel(const __grid_co
     for (; it < nk; ++it) {
       const int s = it % kStages;
       if (it >= kStages && !wait(&ctl->empty[s], ((it / kStages) & 1) ^ 1)) break;
-      if (lane == 0) {
+      if (lane == 0 && !(a.withhold && it == 0)) {
         mbar_arrive_expect_tx(&ctl->full[s], 2 * kOpBytes);
         tma_load_2d(smem + s * kStageBytes, &a.x, &ctl->full[s], (kb + it) * kChunk, t0);
         tma_load_2d(smem + s * kStageBytes + kOpBytes, &a.w, &ctl->full[s], (kb + it) * kChunk, n0);
@@ -303,6 +304,7 @@ cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t str
   p.act = a.act;
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
+  p.withhold = a.withhold;
   const long long tiles = (static_cast<long long>(a.T) + kTile - 1) / kTile * ((a.Cout + kTile - 1) / kTile);
   const int nk = (a.Cin + kChunk - 1) / kChunk;
   // Few tiles: the channels are split, up to one CTA per SM; clusters of 8 up to two thirds of

@@ -58,6 +58,7 @@ struct RowsArgs {
   int T, Cin, Cout, act;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;
 };
 
 struct RowsCtl {
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     // ---------------------------------------------------------------- TMA (one thread)
     if (lane == 0) {
       uint32_t it = 0;
+      const uint32_t skip = a.withhold ? 0u : 0xffffffffu;   // the stage that the test hook withholds
       bool ok = true;
       for (long long tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
         const int t0 = static_cast<int>(tile / ncol) * kM, n0 = static_cast<int>(tile % ncol) * NT;
@@ -123,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             ok = false;
             break;
           }
+          if (it == skip) continue;
           mbar_arrive_expect_tx(&ctl->full[s], kStageBytes);
           tma_load_2d(smem + s * kStageBytes, &a.x, &ctl->full[s], k * kChunk, t0);
           tma_load_2d(smem + s * kStageBytes + kABytes, &a.w, &ctl->full[s], k * kChunk, n0);
@@ -344,6 +347,7 @@ struct SplitArgs {
   int T, Cin, Cout, act;
   unsigned* err;
   unsigned long long wait_limit_ns;
+  bool withhold;
 };
 
 constexpr int kAccs = 4;                           // accumulators in turn for fp32 outputs (256 columns at N = 64: two CTAs fit)
@@ -402,6 +406,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
+      const uint32_t skip = a.withhold ? 0u : 0xffffffffu;
       for (; it < static_cast<uint32_t>(nk); ++it) {
         const uint32_t s = it % kSplitStages, ph = (it / kSplitStages) & 1;
         if (it >= kSplitStages && !mbar_wait_bounded(&ctl->empty[s], ph ^ 1, lim, abortp)) {
@@ -409,6 +414,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
           atomicOr(a.err, kErrTimeout);
           break;
         }
+        if (it == skip) continue;
         mbar_arrive_expect_tx(&ctl->full[s], kBytes);
         tma_load_2d(smem + s * kBytes, &a.w, &ctl->full[s], (kb + static_cast<int>(it)) * kChunk, n0);
         tma_load_2d(smem + s * kBytes + kWBytes, &a.x, &ctl->full[s], (kb + static_cast<int>(it)) * kChunk, t0);
@@ -566,6 +572,7 @@ cudaError_t launch_rows(const LinearArgs& a, int num_sms, cudaStream_t stream, c
   r.act = a.act;
   r.err = a.err;
   r.wait_limit_ns = a.wait_limit_ns;
+  r.withhold = a.withhold;
   const long long tiles = (static_cast<long long>(a.T) + kM - 1) / kM * ((a.Cout + NT - 1) / NT);
   const unsigned grid = static_cast<unsigned>(tiles < num_sms ? tiles : num_sms);
   if (a.out_bf16) return a.residual ? go_rows<NT, false, true>(r, grid, stream) : go_rows<NT, false, false>(r, grid, stream);
@@ -600,6 +607,7 @@ cudaError_t launch_split(const LinearArgs& a, int S, cudaStream_t stream, const 
   p.act = a.act;
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
+  p.withhold = a.withhold;
   const unsigned ctiles = (a.Cout + 127) / 128, rtiles = (static_cast<unsigned>(a.T) + N - 1) / N;
   return a.out_bf16 ? go_split<N, __nv_bfloat16>(p, S, ctiles, rtiles, stream)
                     : go_split<N, float>(p, S, ctiles, rtiles, stream);

@@ -131,3 +131,61 @@ def test_attention_scores_beyond_32_bits(case, sign):
     ref = torch.where((win == 0)[..., None], (ref + vs[:, Tk - 1:Tk]) / 2, ref)
     clear = clear.permute(0, 2, 1)
     check(out[clear], ref[clear], (unit(dt) * ref.abs() + 2.0 ** -22 * (vs.abs().amax(1, keepdim=True)))[clear], "best key's value")
+
+
+# ------------------------------------------------------------------ waits that run out
+def linear_call(T, Cin, Cout, dt, odt, res):
+    x, w, b = rand(1, T, Cin, dt=dt), rand(2, Cout, Cin, dt=dt, std=Cin ** -0.5), rand(3, Cout)
+    r = rand(4, T, Cout, dt=odt) if res else None
+    out = torch.empty(T, Cout, dtype=DT[odt][0], device="cuda")
+
+    def call():
+        gk.gkd_linear(x, DT[dt][1], T, Cin, Cin, w, Cout, b, gk.GKD_ACT_GELU, None, r, Cout, out, DT[odt][1], Cout)
+        return out
+    return call
+
+
+def attention_call(B, Tq, Tk, H, Hk, D, dt, causal, masked):
+    q, k, v = (rand(i, *s, dt=dt) for i, s in ((1, (B, Tq, H, D)), (2, (B, Tk, Hk, D)), (3, (B, Tk, Hk, D))))
+    mask = (torch.rand(B, Tk, generator=torch.Generator().manual_seed(4)) < 0.7).to(torch.uint8).cuda() if masked else None
+    out = torch.empty_like(q)
+
+    def call():
+        gk.gkd_attention(q, k, v, DT[dt][1], B, Tq, Tk, D, D ** -0.5, causal, mask, Tk, out)
+        return out
+    return call
+
+
+WAITS = [
+    # the kernel for many rows (each width, both output types, a residual on its way), the one for few (alone, in clusters)
+    (linear_call, 5000, 72, 1032, "bf16", "bf16", True), (linear_call, 1360, 520, 808, "bf16", "f32", True),
+    (linear_call, 9400, 520, 1024, "bf16", "f32", False), (linear_call, 17, 1280, 2048, "bf16", "bf16", False),
+    (linear_call, 64, 8192, 136, "bf16", "f32", True), (linear_call, 200, 128, 1032, "bf16", "bf16", True),
+    (linear_call, 17, 1280, 520, "f32", "f32", True), (linear_call, 1360, 264, 1024, "f32", "f32", False),
+    # heads of one and two chunks, with and without a mask, one CTA and clusters per query tile
+    (attention_call, 2, 300, 300, 8, 4, 64, "bf16", 0, False), (attention_call, 2, 300, 300, 8, 8, 128, "bf16", 1, True),
+    (attention_call, 1, 1, 2304, 4, 4, 64, "bf16", 0, True), (attention_call, 1, 130, 1500, 2, 1, 128, "bf16", 0, False),
+    (attention_call, 2, 300, 300, 8, 4, 64, "f32", 0, False), (attention_call, 2, 300, 300, 8, 8, 128, "f32", 1, True),
+    (attention_call, 1, 40, 2304, 4, 4, 64, "f32", 0, True), (attention_call, 1, 130, 1500, 2, 1, 128, "f32", 0, False),
+]
+
+
+@pytest.mark.parametrize("case", WAITS, ids=lambda c: "-".join(str(v) for v in (c[0].__name__, *c[1:])))
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(case):
+    call = case[0](*case[1:])
+    want = call().clone()
+    settle()
+    gk.gkd_set_wait_timeout_ms(50)
+    try:
+        gk.gkd_debug_set_flags(gk.DEBUG_SKIP_PRODUCER_ARRIVE)
+        call()
+        with pytest.raises(gk.GkdError) as e:
+            gk.gkd_check_device_error()
+        assert e.value.status == gk.GKD_ERR_TIMEOUT
+    finally:
+        gk.gkd_debug_set_flags(0)
+        gk.gkd_set_wait_timeout_ms(2000)
+    call().fill_(777.0)
+    got = call()
+    settle()
+    assert torch.equal(got, want)
