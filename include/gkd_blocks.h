@@ -138,9 +138,11 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  * exponentials in fp32; the weights p_j are rounded to bf16 for the product with v
  * (their sum is not). dt = GKD_F32: every operand as three bf16 numbers (24 bits), six
  * products per term, the rest in fp32 (up to 24 keys or 16 queries: fp32 fused
- * multiply-adds); visible values must be finite and below 2^127 in magnitude (others can
- * give NaN, and so can scores that overflow). A score of -inf has weight 0 beside larger
- * ones. A row with a score of NaN or +inf is NaN, and so is one whose scores are all -inf.
+ * multiply-adds); visible q, k and v must be finite and below 2^127 in magnitude (others
+ * can give NaN, and so can scores that overflow). The sum of p_j v is formed before its
+ * division: values of one sign above 2^127 / Tk (bf16: 2^119 / Tk) can overflow in it.
+ * A score of -inf has weight 0 beside larger ones. A row with a score of NaN or +inf is
+ * NaN, and so is one whose scores are all -inf.
  * Limits: 0 <= B <= 65535, 0 <= Tq, Tk < 2^31 - 256, 8 <= D <= 128, D % 8 == 0,
  * 1 <= heads <= 1024, scale finite and positive.
  */
