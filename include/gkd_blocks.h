@@ -137,8 +137,8 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  * dt = GKD_BF16: tensor-core products with fp32 accumulation; maxima, sums and
  * exponentials in fp32; the weights p_j are rounded to bf16 for the product with v
  * (their sum is not). dt = GKD_F32: every operand as three bf16 numbers (24 bits), six
- * products per term, the rest in fp32 (up to 24 keys or 16 queries: fp32 fused
- * multiply-adds); visible q, k and v must be finite and below 2^127 in magnitude (others
+ * products per term, the rest in fp32 (up to 24 keys or 12 queries, and 16 where that is
+ * faster: fp32 fused multiply-adds); visible q, k and v must be finite and below 2^127 in magnitude (others
  * can give NaN, and so can scores that overflow). The sum of p_j v is formed before its
  * division: values of one sign above 2^127 / Tk (bf16: 2^119 / Tk) can overflow in it.
  * A score of -inf has weight 0 beside larger ones. A row with a score of NaN or +inf is

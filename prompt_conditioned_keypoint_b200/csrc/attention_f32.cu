@@ -668,7 +668,7 @@ cudaError_t go(const AttentionArgs& a, cudaStream_t stream) {
 // kernel, which has 128 rows whatever it gets, in brackets): 57 batches of 20 heads of 64 over 4358 keys with
 // holes 222 / 581 / 1112 (1502 to 1506), 64 of 16 heads over 581 55.5 / 111 / 217 (254), one batch over
 // 2304 9.1 / 13.7 / 16.1 (28), 8 of 8 heads of 128 over 581 8.4 / 15.7 / 27.7 (37 to 39), 16 batches of
-// 16 heads on 4 key heads 10.0 / 25.8 / 51 (70). The time grows with the tiles of four rows: from about 20 queries on the tensor cores are faster.
+// 16 heads on 4 key heads 10.0 / 25.8 / 51 (70). The time grows with the tiles of four rows; fits() below has the other side.
 namespace att32rows {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32, NP = 4, U = 2;
@@ -869,6 +869,21 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
   if (S > 1) cluster_sync();                        // nobody leaves while its shared memory is read
 }
 
+// Up to 12 queries always (2 to 12 took 0.12 to 1.00 of the tensor-core kernel's time over 25 to 400 keys, alone or on
+// shared heads, 16 to 1024 heads in the batch), and so 16 over long rows of keys or where the tiles of four rows are one
+// wave of CTAs (0.43 to 0.72). Between, those tiles read all keys for less work than that costs: 13 to 16 queries of 1024
+// heads of 64 took 1.21 of its time over 25 keys, 1.14 over 48, 1.31 over 128, 1.12 over 256, 0.93 over 400; on shared heads
+// 0.98 and 1.21 (13 and 16) over 25 to 128 keys, 0.88 and 1.08 over 192. Heads of 128, 1024 of them: 0.83 over 32 keys, 0.97
+// over 48, 1.09 over 64, 1.15 over 128, 1.02 over 192, 0.95 over 256; on shared heads 0.68 to 1.01; 80 and 128 of them
+// 0.83 to 1.01.
+bool fits(const AttentionArgs& a, int num_sms) {
+  if (a.Tq > 16) return false;
+  const long long group = a.q.heads / a.k.heads, tiles = (a.Tq * group + 3) / 4 * a.k.heads * a.B;
+  if (a.Tq <= 12 || tiles <= 2 * num_sms) return true;
+  if (a.D <= 64) return a.Tk > (group > 1 ? 128 : 256);
+  return group > 1 || tiles <= 8 * num_sms || a.Tk <= 48 || a.Tk > 192;
+}
+
 template <int L, int R>
 cudaError_t go(const AttentionArgs& a, int num_sms, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.Tq) * (a.q.heads / a.k.heads);
@@ -885,8 +900,7 @@ cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream
   if (a.Tk <= 8) return att32few::go<8>(a, stream);
   if (a.Tk <= 16) return att32few::go<16>(a, stream);
   if (a.Tk <= 24) return att32few::go<24>(a, stream);
-  // few rows, whatever the number of keys: fma units (both sides beside that kernel)
-  if (a.Tq <= 16) {
+  if (att32rows::fits(a, num_sms)) {
     using namespace att32rows;
     if (a.Tq == 1 && a.q.heads == a.k.heads) return a.D <= 64 ? go<4, 1>(a, num_sms, stream) : go<8, 1>(a, num_sms, stream);
     return a.D <= 64 ? go<4, 4>(a, num_sms, stream) : go<8, 4>(a, num_sms, stream);

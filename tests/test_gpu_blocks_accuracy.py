@@ -78,3 +78,21 @@ def test_linear_keeps_an_infinity_to_its_own_row_and_column(T):
     cols = [i for i in range(Cout) if i not in (7, 9)]
     assert not torch.isfinite(out[1]).any() and not torch.isfinite(out[:, [7, 9]]).any()
     check(out[rows][:, cols], ref[rows][:, cols], tol[rows][:, cols], "the rest")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Tq,Tk,Hk", [(12, 100, 8), (13, 30, 8), (13, 49, 2), (16, 128, 2), (16, 129, 2), (16, 192, 8), (14, 193, 8),
+                                      (16, 256, 8), (15, 257, 8)])
+def test_attention_of_up_to_16_rows_in_a_batch_that_fills_the_gpu(Tq, Tk, Hk, D):
+    """Both kernels that take 13 to 16 rows, and each end of the rule between them."""
+    B, H = 40, 8
+    q, k, v = rand(1, B, Tq, H, D, std=2.0), rand(2, B, Tk, Hk, D), rand(3, B, Tk, Hk, D)
+    mask = (torch.rand(B, Tk, generator=torch.Generator().manual_seed(4)) < 0.6).to(torch.uint8).cuda()
+    mask[3] = 0
+    ref, tol = attention_ref(q, k, v, D ** -0.5, 1, mask, "f32")
+    k[mask == 0], v[mask == 0] = math.nan, math.inf
+    out = torch.full_like(q, 777.0)
+    gk.gkd_attention(q, k, v, gk.GKD_F32, B, Tq, Tk, D, D ** -0.5, 1, mask, Tk, out)
+    settle()
+    check(out, ref, tol, "up to 16 rows")
+    assert not out[3].any()
