@@ -65,11 +65,6 @@ struct Plan {
 // parity of the tile: a softmax warp may be a tile ahead of another.
 constexpr uint32_t kColP = 128, kColO = 320;
 
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t lbo) {
-  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-
 // Two values as their planes' bf16 pairs.
 __device__ __forceinline__ void planes(float x, float y, uint32_t (&p)[3]) {
 #pragma unroll
@@ -209,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);        // and N = the keys taken
       const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
       const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(kv));
-      const uint64_t vd = desc_mn_sw128(smem_u32(kv) + P::kKvBytes, BN * 128);
+      const uint64_t vd = umma_desc_mn_sw128(smem_u32(kv) + P::kKvBytes, BN * 128);
       bool issued = false;
       auto scores = [&](uint32_t j, int words) {
         const uint32_t s = j % kStages;

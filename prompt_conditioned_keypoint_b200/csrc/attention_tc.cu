@@ -80,13 +80,6 @@ struct Ctl {
   float m[kRows], l[kRows];                         // of the rows, for the other CTAs of the cluster
 };
 
-// Descriptor of V for the second product: the 64-column chunk of a key row is contiguous
-// (MN-major, 128B swizzle); 8 key rows to 1024 bytes (SBO), chunks `lbo` bytes apart.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t lbo) {
-  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-
 template <int DCH, bool MASK>
 __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(const __grid_constant__ Args a, int S) {
   constexpr int kBufs = DCH;                                         // buffers of scores
@@ -253,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);        // and N = the keys taken
     const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(dk * 2) << 17) | (8u << 24);
     const uint64_t qd = umma_desc_sw128(smem_u32(smem)), kd = umma_desc_sw128(smem_u32(ks));
-    const uint64_t vd = desc_mn_sw128(smem_u32(vs), BN * 128);
+    const uint64_t vd = umma_desc_mn_sw128(smem_u32(vs), BN * 128);
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool okw = mbar_wait_bounded(bar, parity, lim, abortp);
