@@ -144,7 +144,7 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  * A score of -inf has weight 0 beside larger ones. A row with a score of NaN or +inf is
  * NaN, and so is one whose scores are all -inf.
  * Limits: 0 <= B <= 65535, 0 <= Tq, Tk < 2^31 - 256, 8 <= D <= 128, D % 8 == 0,
- * 1 <= heads <= 1024, scale finite and positive.
+ * 1 <= heads <= 1024, 0 < scale < 2^127.
  */
 GKD_API gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads* v, gkd_dtype dt, int B,
                                  int Tq, int Tk, int D, float scale, int causal, const uint8_t* key_mask,

@@ -125,6 +125,13 @@ gkd_status launched(cudaError_t e, const char* what) {
 
 namespace gkd {
 
+ScoreScale score_scale(float scale) {
+  const float c = scale * 1.4426950408889634f;
+  int e = 0;
+  std::frexp(c, &e);                                 // c = f 2^e, 0.5 <= f < 1
+  return ScoreScale{c, std::ldexp(1.f, e - 1), std::ldexp(1.f, 31 - e)};
+}
+
 EncodeTiledFn get_encode_tiled() {
   static EncodeTiledFn fn = [] {
     void* p = nullptr;
@@ -715,7 +722,7 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   constexpr int kMaxRows = 0x7fffffff - 256;
   if (Tq < 0 || Tk < 0 || Tq > kMaxRows || Tk > kMaxRows) return fail(GKD_ERR_SHAPE, "Tq=%d Tk=%d out of range", Tq, Tk);
   if (D < 8 || D > 128 || D % 8) return fail(GKD_ERR_SHAPE, "D=%d must be a multiple of 8 in [8, 128]", D);
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GKD_ERR_ARG, "scale must be positive and finite");
+  if (!(scale > 0.f) || !(scale < 0x1p127f)) return fail(GKD_ERR_ARG, "scale must be positive and below 2^127");
   if (causal != 0 && causal != 1) return fail(GKD_ERR_ARG, "causal must be 0 or 1");
   if (key_mask_batch_stride < 0) return fail(GKD_ERR_SHAPE, "key_mask_batch_stride must not be negative");
   GKD_TRY(check_head_count("q", q));
@@ -751,8 +758,8 @@ gkd_status gkd_attention(const gkd_heads* q, const gkd_heads* k, const gkd_heads
   a.Tq = Tq;
   a.Tk = Tk;
   a.D = D;
-  a.causal = causal;
-  a.scale = scale;
+  a.causal = causal != 0;
+  a.scale = gkd::score_scale(scale);
   a.mask = key_mask;
   a.mask_batch_stride = key_mask_batch_stride;
   a.err = ds->err_word;

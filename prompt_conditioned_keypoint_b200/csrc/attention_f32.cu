@@ -52,7 +52,7 @@ struct Plan {
     uint64_t qready, kready[kStages], kempty[kStages], vready[kStages], vempty[kStages];
     uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], odone[2], drain;
     Info info[kInfo];
-    int first;                                      // the first key that the mask leaves in this CTA's tiles
+    int first;                                      // the first key that the mask leaves in this CTA's tiles (none: INT_MAX)
     uint32_t tmem_base;
     int abort_flag;
     float m[kRows], l[kRows];                       // of the rows, for the other CTAs of the cluster
@@ -90,8 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
   const int bh = work / ntiles, h = bh % a.q.heads, b = bh / a.q.heads, hk = h / (a.q.heads / a.k.heads);
   const int r0 = tile * kRows;
   const long long shift = static_cast<long long>(a.Tk) - a.Tq;     // causal: key j for row i iff j <= i + shift
-  const float scale_log2 = a.scale * 1.4426950408889634f;
-  const ScoreScale ss = score_scale(scale_log2);
+  const float scale_log2 = a.scale.c;
   const int dk = (a.D + 15) / 16;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abortp = &ctl->abort_flag;
@@ -107,6 +106,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
       atomicOr(a.err, kErrTimeout);
     }
   };
+
+  // What a row's output is multiplied by whose sum is 0, having no score above -inf: 0 without a key, but 0 / 0 if it
+  // sees one, of score -inf.
+  auto empty = [&](int first, int r) { return first <= (a.causal ? r0 + r + shift : static_cast<long long>(a.Tk)) ? NAN : 0.f; };
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->qready, kConvThreads / 32);
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
+    ctl->first = 0x7fffffff;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < BN; e += 2) t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], x[e], x[e + 1]);
       const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], m);   // NaN if any score was
-      const float factor = ss.factor(top), base = ss.offset(top);
+      const float factor = score_factor(a.scale, top), base = score_offset(a.scale, top);
       const float f = m == -INFINITY ? 0.f : ex2_approx((m - top) * scale_log2);
       m = top;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -355,11 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
     if (ok && j > 0 && active) gather(j - 1, 1.f);
     if (S > 1 && j == 0) wait(&ctl->qready, 0);     // no tile: Q's planes, which the share overwrites, may still be written
     if (!ok) give_up();
-    // No score above -inf: a row that sees a key all the same is 0 / 0, one without a key is 0. Their sums are
-    // both 0 so far; 1 marks the first.
-    if (ok && j > 0 && m == -INFINITY && (!a.causal || ctl->first <= r0 + r + shift)) l = 1.f;
     if (S == 1) {
-      const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
+      const float inv = l == 0.f ? empty(ctl->first, r) : 1.f / l;
       float* o = static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride;
       if (ok && r0 + r < a.Tq) {
 #pragma unroll
@@ -479,10 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_f32_kernel(const __grid
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      if (top == -INFINITY)                         // no score above -inf in any share: their marks
+      float inv = 1.f / l;
+      if (l == 0.f) {
+        int first = 0x7fffffff;
 #pragma unroll 1
-        for (int s = 0; s < S; ++s) l += cluster_load1(cluster_map(ol + 4 * r, s));
-      const float inv = l == 0.f ? 0.f : top == -INFINITY ? NAN : 1.f / l;
+        for (int s = 0; s < S; ++s)
+          first = min(first, __float_as_int(cluster_load1(cluster_map(smem_u32(&ctl->first), s))));
+        inv = empty(first, r);
+      }
       store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + (r0 + r) * a.out.row_stride + h * a.out.head_stride + 4 * c,
              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
@@ -560,7 +565,6 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
   __syncthreads();
   if (static_cast<long long>(tile) * kRows + (threadIdx.x >> 5) * 8 >= a.Tq) return;   // a warp without a row
 
-  const ScoreScale ss = score_scale(a.scale * 1.4426950408889634f);
   float w[R][KMAX], inv[R];
 #pragma unroll
   for (int j0 = 0; j0 < KMAX; j0 += 4) {            // four keys at a time: their sums in flight together
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kThreads) attention_few_keys_kernel(const __gr
       w[i][j + 1] = (bits >> (j + 1)) & 1u ? w[i][j + 1] : -INFINITY;
       top = max3_nan(top, w[i][j], w[i][j + 1]);    // NaN if any score was
     }
-    const float factor = ss.factor(top), base = ss.offset(top);
+    const float factor = score_factor(a.scale, top), base = score_offset(a.scale, top);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
@@ -683,8 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
   const float* k = static_cast<const float*>(a.k.data) + b * a.k.batch_stride + hk * a.k.head_stride;
   const float* v = static_cast<const float*>(a.v.data) + b * a.v.batch_stride + hk * a.v.head_stride;
   const uint8_t* mask = a.mask ? a.mask + b * a.mask_batch_stride : nullptr;
-  const float scale_log2 = a.scale * 1.4426950408889634f;
-  const ScoreScale ss = score_scale(scale_log2);
+  const float scale_log2 = a.scale.c;
 
   for (int i = threadIdx.x; i < R * kRow; i += kThreads) {
     const long long u = static_cast<long long>(tile) * R + i / kRow;
@@ -765,13 +768,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       if (top != m[r]) {
         const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
         m[r] = top;
-        base[r] = ss.offset(top);
+        base[r] = score_offset(a.scale, top);
         l[r] *= f;
 #pragma unroll
         for (int c = 0; c < NP; ++c)
           acc[r][c] = make_float4(acc[r][c].x * f, acc[r][c].y * f, acc[r][c].z * f, acc[r][c].w * f);
       }
-      const float factor = ss.factor(top);
+      const float factor = score_factor(a.scale, top);
 #pragma unroll
       for (int e = 0; e < U; ++e) {
         const float p = ex2_approx(fmaf(s[r][e], factor, -base[r]));

@@ -54,13 +54,13 @@ struct Args {
   long long out_bs, out_rs, out_hs;
   int heads, group;                                 // query heads, query heads per key head
   int kb_shared;                                    // bit 0: q, 1: k, 2: v has one batch for all
-  int Tq, Tk, D, causal, ntiles;
-  float scale_log2;                                 // scale * log2(e)
+  int Tq, Tk, D, ntiles;
+  bool causal, withhold;
+  ScoreScale scale;
   const uint8_t* mask;                              // MASK kernels
   long long mask_bs;
   unsigned* err;
   unsigned long long wait_limit_ns;
-  bool withhold;
 };
 
 struct Info {                                       // one key tile
@@ -74,7 +74,7 @@ struct Ctl {
   uint64_t qfull, kfull[kKvStages], kempty[kKvStages], vfull[kKvStages], vempty[kKvStages];
   uint64_t ifull[kInfo], iempty[kInfo], sfull[2], pready[2], pvdone, odone, drain;
   Info info[kInfo];
-  int first;                                        // the first key that the mask leaves in this CTA's tiles
+  int first;                                        // the first key that the mask leaves in this CTA's tiles (none: INT_MAX)
   uint32_t tmem_base;
   int abort_flag;
   float m[kRows], l[kRows];                         // of the rows, for the other CTAs of the cluster
@@ -118,6 +118,12 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
   if (a.causal) full = max(0ll, min(full, r0 + shift + 1));
   const int seen = static_cast<int>(full / BN);
 
+  // What a row's output is multiplied by whose sum is 0, having no score above -inf: 0 without a key, but 0 / 0 if it
+  // sees one, of score -inf.
+  auto empty = [&](int first, int r) {
+    return first <= (a.causal ? r0 + r + static_cast<long long>(a.Tk) - a.Tq : static_cast<long long>(a.Tk)) ? NAN : 0.f;
+  };
+
   if (threadIdx.x == 0) {
     mbar_init(&ctl->qfull, 1);
     for (int s = 0; s < kKvStages; ++s) {
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     mbar_init(&ctl->odone, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
-    ctl->first = lo * BN;                           // with a mask set anew
+    ctl->first = MASK || lo >= hi ? 0x7fffffff : lo * BN;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -398,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
             t4[(e >> 1) & 3] = max3_nan(t4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         }
         const float top = max3_nan(max3_nan(t4[0], t4[1], t4[2]), t4[3], t4[3]);   // NaN if any score is
-        const bool grow = !((top - m) * a.scale_log2 <= kGrow);   // also for NaN, and where there was no key before
+        const bool grow = !((top - m) * a.scale.c <= kGrow);   // also for NaN, and where there was no key before
         if (__any_sync(0xffffffffu, grow)) {
           float mn = max3_nan(m, top, top);
           if (mn == INFINITY) mn = NAN;               // infinity against infinity: the row is NaN
-          const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
+          const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale.c);
           m = mn;
           l *= f;
           if (j > 0) {
@@ -421,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
             }
           }
         }
-        const ScoreScale ss = score_scale(a.scale_log2);
-        const float factor = ss.factor(m), base = ss.offset(m);
+        const float factor = score_factor(a.scale, m), base = score_offset(a.scale, m);
         const float2 scale2 = make_float2(factor, factor), base2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         if (!kHold) load(0);
@@ -469,10 +474,6 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
     }
     if (!ok && lane == 0) give_up();
     const bool mine = ok && r0 + r < a.Tq;
-    // No score above -inf: a row that sees a key all the same is 0 / 0, one without a key is 0. Their sums are
-    // both 0 so far; 1 marks the first.
-    if (ok && j > 0 && m == -INFINITY && (!a.causal || ctl->first <= r0 + r + static_cast<long long>(a.Tk) - a.Tq)) l = 1.f;
-    const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs;
     if (S > 1) {
       ctl->m[r] = m;
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
       }
       if (S == 1) {
         if (!mine) continue;
+        const float inv = l == 0.f ? empty(ctl->first, r) : 1.f / l;
 #pragma unroll
         for (int e = 0; e < 16; e += 8) {
           if (16 * c + e >= a.D) continue;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
 #pragma unroll 8
       for (int s = 0; s < S; ++s) {
         const float ms = cluster_load1(cluster_map(om + 4 * r, s));
-        const float f = ms == -INFINITY ? 0.f : ex2_approx((ms - m) * a.scale_log2);   // 0: a share without a key for this row
+        const float f = ms == -INFINITY ? 0.f : ex2_approx((ms - m) * a.scale.c);   // 0: a share without a key for this row
         const float4 v = cluster_load4(cluster_map(oo + r * (256 * DCH) + ((c ^ (r & 15)) << 4), s));
         l = fmaf(f, cluster_load1(cluster_map(ol + 4 * r, s)), l);
         o.x = fmaf(f, v.x, o.x);
@@ -537,10 +539,14 @@ __global__ void __launch_bounds__(kThreads, DCH == 1 ? 4 : 2) attention_kernel(c
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
       }
-      if (m == -INFINITY)                           // no score above -inf in any share: their marks
+      float inv = 1.f / l;
+      if (l == 0.f) {
+        int first = 0x7fffffff;
 #pragma unroll 1
-        for (int s = 0; s < S; ++s) l += cluster_load1(cluster_map(ol + 4 * r, s));
-      const float inv = l == 0.f ? 0.f : m == -INFINITY ? NAN : 1.f / l;
+        for (int s = 0; s < S; ++s)
+          first = min(first, __float_as_int(cluster_load1(cluster_map(smem_u32(&ctl->first), s))));
+        inv = empty(first, r);
+      }
       store4(static_cast<__nv_bfloat16*>(a.out) + b * a.out_bs + (r0 + r) * a.out_rs + h * a.out_hs + 4 * c,
              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
@@ -609,7 +615,7 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_
   p.D = a.D;
   p.causal = a.causal;
   p.ntiles = static_cast<int>((static_cast<long long>(a.Tq) + kRows - 1) / kRows);
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale = a.scale;
   p.mask = a.mask;
   p.mask_bs = a.mask_batch_stride;
   p.err = a.err;

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "gkd_internal.h"
 #include "ptx.cuh"
 
 namespace gkd {
@@ -23,19 +24,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// A row's weights are 2^(s f - m f) for its scores s and the largest of them m, by one fused multiply-add on the rounded
-// m f, with f = c = scale log2(e). That rounding, common to the row's weights, takes them out of the exponent's range
-// once |m c| passes 2^31. But from |m| pow2 = 2^30 on, pow2 the power of two below c, the scores next to m are 2^6 and
-// more away from it (in units of 1 / pow2): whatever is below m has no weight, and f = pow2, with which m f is exact,
-// serves as well.
-struct ScoreScale {
-  float c, pow2, far;
-  __device__ __forceinline__ float factor(float m) const { return fabsf(m) < far ? c : pow2; }
-  __device__ __forceinline__ float offset(float m) const { return m == -INFINITY ? 0.f : m * factor(m); }   // no key yet: every weight is 0
-};
-__device__ __forceinline__ ScoreScale score_scale(float c) {
-  const uint32_t e = __float_as_uint(c) >> 23;               // pow2 = 2^(e - 127), far = 2^(157 - e); pow2 > 0: -inf times it is -inf
-  return ScoreScale{c, __uint_as_float(max(e << 23, 1u)), __uint_as_float(min(284u - e, 255u) << 23)};
+// The factor on the scores of a row whose largest is m, and what m comes to with it (no key yet: every weight is 0).
+__device__ __forceinline__ float score_factor(const ScoreScale& s, float m) { return fabsf(m) < s.far ? s.c : s.pow2; }
+__device__ __forceinline__ float score_offset(const ScoreScale& s, float m) {
+  return m == -INFINITY ? 0.f : m * score_factor(s, m);
 }
 
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActQuickGelu = 3 };

@@ -157,9 +157,9 @@ struct LinearArgs {
   long long x_stride, residual_stride, out_stride;   // elements between rows
   int T, Cin, Cout, act;
   bool out_bf16;
+  bool withhold;             // test hook: the first stage of every CTA is not handed to the products
   unsigned* err;
   unsigned long long wait_limit_ns;
-  bool withhold;             // test hook: the first stage of every CTA is not handed to the products
 };
 cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream, const char** why);   // bf16 operands
@@ -190,15 +190,27 @@ struct HeadsView {           // element (b, t, h, i) at data + b batch_stride + 
   long long batch_stride, row_stride, head_stride;
   int heads;
 };
+// A row's weights are 2^(s f - m f) for its scores s and the largest of them m, by one fused multiply-add on the rounded
+// m f, with f = c = scale log2(e). That rounding, common to the row's weights, takes them out of the exponent's range
+// once |m c| passes 2^31. But from |m| pow2 = 2^30 on, pow2 the power of two below c, the scores next to m are 2^6 and
+// more away from it (in units of 1 / pow2): whatever is below m has no weight, and f = pow2, with which m f is exact,
+// serves as well. (factor and offset of a row: blocks_common.cuh. Formed here, since code in the kernels that ran once
+// took 0.2 of 13 us of a one-row call.)
+struct ScoreScale {
+  float c, pow2, far;        // far = 2^30 / pow2
+};
+ScoreScale score_scale(float scale);
+
 struct AttentionArgs {
   HeadsView q, k, v, out;
-  int B, Tq, Tk, D, causal;
-  float scale;
+  int B, Tq, Tk, D;
+  bool causal;
+  bool withhold;             // test hook: the first tile of keys of every CTA is not handed to the products
+  ScoreScale scale;
   const uint8_t* mask;       // batch b's [Tk] at mask + b * mask_batch_stride, or null
   long long mask_batch_stride;
   unsigned* err;
   unsigned long long wait_limit_ns;
-  bool withhold;             // test hook: the first tile of keys of every CTA is not handed to the products
 };
 cudaError_t launch_attention_none(const AttentionArgs& a, int size, cudaStream_t stream);   // Tk = 0: zeros
 cudaError_t launch_attention_f32(const AttentionArgs& a, int num_sms, cudaStream_t stream);

@@ -46,10 +46,11 @@ struct Args {
   const float* residual;
   float* out;
   long long residual_stride, out_stride;
-  int T, Cin, Cout, act;
+  int T, Cin, Cout;
+  short act;
+  bool withhold;             // in a word that is read anyway: at the end it was fetched by itself, 0.5 us
   unsigned* err;
   unsigned long long wait_limit_ns;
-  bool withhold;
 };
 
 struct Ctl {
@@ -301,7 +302,7 @@ cudaError_t launch_linear_f32(const LinearArgs& a, int num_sms, cudaStream_t str
   p.T = a.T;
   p.Cin = a.Cin;
   p.Cout = a.Cout;
-  p.act = a.act;
+  p.act = static_cast<short>(a.act);
   p.err = a.err;
   p.wait_limit_ns = a.wait_limit_ns;
   p.withhold = a.withhold;

@@ -44,3 +44,11 @@ def test_every_product_of_the_linear_layer_is_seen(Cin):
     assert bool(((sum(terms) - ref).abs() <= tol).all())
     for lost in range(3):
         assert bool(((sum(terms) - terms[lost] - ref).abs() > 5 * tol).all())
+
+
+def test_a_scale_whose_base_2_form_overflows_is_refused():
+    from prompt_conditioned_keypoint_b200 import binding as gk
+    v = gk.GkdHeads(0x10000, 1 << 12, 1 << 8, 64, 4)
+    for scale, refused in ((2.0 ** 127, True), (3e38, True), (1.7e38, False), (1e-44, False)):
+        status = gk.lib.gkd_attention(v, v, v, gk.GKD_F32, 2, 3, 5, 64, scale, 0, None, 5, v, None)
+        assert ("scale" in gk.gkd_last_error()) == refused and status in (gk.GKD_ERR_CUDA, gk.GKD_ERR_ARG)
