@@ -672,6 +672,20 @@ namespace att32rows {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32, NP = 4, U = 2;
 
+// The first of the keys k0, k0 + step, .. below hi that the mask leaves, or INT_MAX. Out of line: inside the kernel it
+// stood between code that every call runs (0.3 of 10 us); noted in the loop over the keys it took 2% of 5 and 16 rows' time.
+__device__ __noinline__ int first_key(const uint8_t* mask, long long k0, int hi, int step) {
+  for (; k0 < hi; k0 += 8 * step) {
+    uint8_t seen[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) seen[e] = k0 + e * step < hi ? (mask ? mask[k0 + e * step] : 1) : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (seen[e]) return static_cast<int>(k0 + e * step);
+  }
+  return 0x7fffffff;
+}
+
 template <int L, int R>                             // lanes per key, NP pieces of 16 bytes each: D <= 16 L; rows
 __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const __grid_constant__ AttentionArgs a, int S) {
   constexpr int kGroups = kThreads / L, kRow = L * NP;             // pieces of a row
@@ -708,12 +722,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
   const int lo = static_cast<int>(static_cast<long long>(most) * rank / S);
   const int hi = static_cast<int>(static_cast<long long>(most) * (rank + 1) / S);
   const int turns = (hi - lo + kGroups * U - 1) / (kGroups * U);   // the same for all: the shuffles want whole warps
-  float m[R], l[R], base[R];                        // base: of the weights, formed where the maximum changes
+  float m[R], l[R], off[R];                         // off: m, but 0 where there was no key yet; (s - off) c needs no ScoreScale
   float4 acc[R][NP];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
-    l[r] = base[r] = 0.f;
+    l[r] = off[r] = 0.f;
 #pragma unroll
     for (int c = 0; c < NP; ++c) acc[r][c] = zero;
   }
@@ -767,17 +781,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       const float top = max3_nan(m[r], s[r][0], s[r][U - 1]);      // NaN if any score was
       if (top != m[r]) {
         const float f = m[r] == -INFINITY ? 0.f : ex2_approx((m[r] - top) * scale_log2);
-        m[r] = top;
-        base[r] = score_offset(a.scale, top);
+        m[r] = off[r] = top;
         l[r] *= f;
 #pragma unroll
         for (int c = 0; c < NP; ++c)
           acc[r][c] = make_float4(acc[r][c].x * f, acc[r][c].y * f, acc[r][c].z * f, acc[r][c].w * f);
       }
-      const float factor = score_factor(a.scale, top);
 #pragma unroll
       for (int e = 0; e < U; ++e) {
-        const float p = ex2_approx(fmaf(s[r][e], factor, -base[r]));
+        const float p = ex2_approx((s[r][e] - off[r]) * scale_log2);
         l[r] += p;
 #pragma unroll
         for (int c = 0; c < NP; ++c)
@@ -787,16 +799,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
     }
   }
   // A row without a score above -inf may see a key all the same: the first one that the mask leaves in the group.
-  // (Noted in the loop it took 2% of 5 and 16 rows' time.)
   int first = 0x7fffffff;
   bool low = false;
 #pragma unroll
   for (int r = 0; r < R; ++r) low |= m[r] == -INFINITY;
-  if (low) {
-#pragma unroll 1
-    for (int key = lo + group; key < hi && first > key; key += kGroups)
-      if (!mask || mask[key]) first = key;
-  }
+  if (low) first = first_key(mask, lo + group, hi, kGroups);
   // the warp's groups
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -852,13 +859,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_few_rows_kernel(const _
       sum = fmaf(f, lw, sum);
       o = make_float4(fmaf(f, ow.x, o.x), fmaf(f, ow.y, o.y), fmaf(f, ow.z, o.z), fmaf(f, ow.w, o.w));
     }
-    if (top == -INFINITY)                           // none in any warp: 0 / 0 for a row that sees a key, 0 for one without
+    float inv = 1.f / sum;
+    if (sum == 0.f) {                               // no score above -inf in any warp: 0 / 0 for a row that sees a key, 0 for one without
+      float marks = 0.f;
 #pragma unroll 1
       for (int w = 0; w < S * kWarps; ++w) {
         const int own = w % kWarps * R + r;
-        sum += S > 1 ? cluster_load1(cluster_map(ol + 4 * own, w / kWarps)) : pl[own];
+        marks += S > 1 ? cluster_load1(cluster_map(ol + 4 * own, w / kWarps)) : pl[own];
       }
-    const float inv = sum == 0.f ? 0.f : top == -INFINITY ? NAN : 1.f / sum;
+      inv = marks > 0.f ? NAN : 0.f;
+    }
     store4(static_cast<float*>(a.out.data) + b * a.out.batch_stride + u / g * a.out.row_stride + (hk * g + u % g) * a.out.head_stride +
                4 * c,
            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
