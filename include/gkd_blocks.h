@@ -69,12 +69,15 @@ typedef struct gkd_heads {
  *   bias      [Cout] fp32, or NULL (0)
  *   scale     [Cout] fp32, or NULL (1)
  *   residual  [T][Cout] of type out_dt, rows residual_stride apart, or NULL (0).
- *             It may be `out` itself (with the same stride).
+ *             It may be `out` itself (with the same stride), and must not overlap it
+ *             otherwise.
  *   out       [T][Cout], rows out_stride apart, out_dt = GKD_BF16 or GKD_F32
  *             (dt = GKD_F32 takes GKD_F32 only). Columns past Cout are left alone.
- * dt = GKD_BF16: exact products, sums in fp32. dt = GKD_F32: every operand as a pair
- * of TF32 numbers, three products per term, each term within 2^-19 of its
- * product; x and weight must be finite (an infinity gives NaN). The epilogue is in
+ * dt = GKD_BF16: exact products, sums in fp32 (for an fp32 output at most 512 channels
+ * at a time on the tensor core, whose sums truncate). dt = GKD_F32: every operand as a
+ * pair of TF32 numbers, three products per term, each term within 2^-19 of its product
+ * (on average 1.5e-7 short of it); x and weight must be finite (an infinity gives NaN
+ * or an infinity in its own row or column). The epilogue is in
  * fp32, with one rounding to out_dt. `out` must not overlap x or weight.
  * Limits: 0 <= T < 2^31, 8 <= Cin, Cout <= 65536, both multiples of 8, strides
  * at least the row's length.
@@ -104,7 +107,8 @@ GKD_API gkd_status gkd_linear(const void* x, gkd_dtype dt, int T, int Cin, long 
  *               taken as axis 0.
  *   pair_freq   [pairs] fp32, radians per unit of position
  *   q_out, k_out  as q and k (the same head counts). Each may be its input itself,
- *               with the same strides, and must not overlap it otherwise.
+ *               with the same strides, and must not overlap anything else of the call
+ *               (q_out not k, k_out not q, nor one the other).
  * Angles are formed and reduced in fp64 (positions up to 2^24 keep fp32 accuracy),
  * everything else in fp32, rounded once to dt.
  * Limits: 0 <= B <= 65535, 0 <= T < 2^31, 8 <= D <= 256, D % 8 == 0, 1 <= heads <= 1024,

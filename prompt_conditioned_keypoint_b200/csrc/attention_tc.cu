@@ -29,11 +29,12 @@
 // The weights are rounded to bf16 for the second product (the operand type); their
 // sum l is taken from the fp32 values.
 //
-// Measured (B200, in a graph): 8 x 2309 rows of 20 heads of 64 336 us = 650 TFLOP/s; 12
-// heads of 128 273 us = 961; 64 x 80 rows over 576 keys 38.6 us; one row over 2304 keys
+// Measured (B200, in a graph): 8 x 2309 rows of 20 heads of 64 332 us = 658 TFLOP/s; 12
+// heads of 128 276 us = 950; 64 x 80 rows over 576 keys 38.7 us; one row over 2304 keys
 // 11.4 us. Bound by the chain's instructions and latencies: on 2 x 2309 rows the
-// exponentials keep the special-function unit 45% busy, the tensor pipe is at 22%, 45% of
-// the issue slots are taken. Tried and slower for heads of 64: tiles of 128 keys at two
+// exponentials keep the special-function unit 53% busy, the tensor pipe is at 27%, 44% of
+// the issue slots are taken (heads of 128: 42%, 43%, 36%). Heads up to 64 spill 12 bytes a
+// thread in 80 registers, 16 with a mask. Tried and slower for heads of 64: tiles of 128 keys at two
 // CTAs per SM (394 to 420 us in six forms: one or two threads per row, weights beside the
 // scores, a share of the exponentials on the fma units, 200 registers by giving up the
 // others'); scores held in registers at three CTAs per SM (406 us).
