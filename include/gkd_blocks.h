@@ -144,7 +144,9 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads* q, const gkd_heads* k, gkd_
  * products per term, the rest in fp32 (up to 24 keys or 12 queries, and 16 where that is
  * faster: fp32 fused multiply-adds); visible q, k and v must be finite and below 2^127 in magnitude (others
  * can give NaN, and so can scores that overflow). The sum of p_j v is formed before its
- * division: values of one sign above 2^127 / Tk (bf16: 2^119 / Tk) can overflow in it.
+ * division: values of one sign above 2^127 / Tk (bf16: 2^119 / Tk) can overflow in it,
+ * and above 2^55 / Tk where scale * score passes 2^24 (the rounding of the largest one
+ * is common to a row's weights, and 2^64 at most).
  * A score of -inf has weight 0 beside larger ones. A row with a score of NaN or +inf is
  * NaN, and so is one whose scores are all -inf.
  * Limits: 0 <= B <= 65535, 0 <= Tq, Tk < 2^31 - 256, 8 <= D <= 128, D % 8 == 0,
